@@ -22,6 +22,7 @@ import threading
 __all__ = [
     "FILL", "OPTIONS", "GemmError", "lib", "library_path", "gemm_f32", "gemm_bf16", "plan_f32", "plan_bf16",
     "device_status", "selftest_bounded_wait", "testing_set_hooks", "status_string", "build",
+    "layer_norm", "layer_norm_backward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -114,7 +115,8 @@ def _bind(l):
     l.gemm_testing_host_policy.restype = I
     l.gemm_testing_host_streams.argtypes = [I, I, I]
     l.gemm_testing_host_streams.restype = I
-    return l
+    from . import training
+    return training.bind(l)
 
 
 def lib():
@@ -568,3 +570,6 @@ def f32_wide_rows(M: int, N: int, K: int, sms: int = 152, mode: int = -1) -> int
     if r < 0:
         raise ValueError("invalid arguments")
     return r
+
+
+from .training import layer_norm, layer_norm_backward  # noqa: E402  (training calls back into this module)

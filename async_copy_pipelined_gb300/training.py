@@ -1,0 +1,256 @@
+"""Operators around a projection that is being trained (``include/pipelined_train.h``).
+
+    y, mean, rstd = pg.layer_norm(x, weight, bias, stats=True)
+    C = pg.gemm_bf16(y, W)                                       # the projection itself
+    dx, dweight, dbias = pg.layer_norm_backward(dy, x, mean, rstd, weight)
+
+Argument checks and marshalling only; the kernels are in the CUDA library.
+CUDA tensors in, CUDA tensors out, enqueued on `stream` (default: torch's
+current stream) without synchronising.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import async_copy_pipelined_gb300 as _pg
+
+__all__ = ["layer_norm", "layer_norm_backward"]
+
+F32, BF16 = 0, 1  # enum gemm_dtype
+
+_workspaces = {}
+
+
+def bind(l):
+    I, L, P, F, S = ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p, ctypes.c_float, ctypes.c_size_t
+    l.layer_norm.argtypes = [I, I, P, L, I, P, P, I, P, L, P, P, F, P]
+    l.layer_norm.restype = I
+    l.layer_norm_backward_workspace.argtypes = [I, I, ctypes.POINTER(S)]
+    l.layer_norm_backward_workspace.restype = I
+    l.layer_norm_backward.argtypes = [I, I, P, L, P, L, I, P, P, P, I, P, L, P, P, P, S, P]
+    l.layer_norm_backward.restype = I
+    return l
+
+
+def _dtype(t, name):
+    import torch
+    if t.dtype == torch.float32:
+        return F32
+    if t.dtype == torch.bfloat16:
+        return BF16
+    raise TypeError(f"{name} must be float32 or bfloat16, not {t.dtype}")
+
+
+def _rows(t, name):
+    """(rows, cols, pitch) of a tensor seen as rows of its last dimension:
+    the rows' elements contiguous, the rows at one common distance."""
+    if t.dim() == 0:
+        raise ValueError(f"{name} needs at least one dimension")
+    cols = t.shape[-1]
+    if cols < 1:
+        raise ValueError(f"{name} has empty rows")
+    if t.dim() == 1:
+        rows, pitch = 1, cols
+    elif t.dim() == 2:
+        rows, pitch = t.shape[0], t.stride(0)
+    else:
+        rows = t.numel() // cols
+        pitch = t.stride(-2)
+        if rows > 0:
+            step = pitch * t.shape[-2]
+            for d in range(t.dim() - 3, -1, -1):
+                if t.shape[d] != 1:
+                    if t.shape[-2] == 1 and step == pitch:
+                        pitch = step = t.stride(d)  # the rows' distance is this dimension's
+                    elif t.stride(d) != step:
+                        raise ValueError(f"the rows of {name} must lie at one common distance")
+                    step = t.stride(d) * t.shape[d]
+    if rows == 0:
+        return 0, cols, cols
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit column stride (row-major rows)")
+    if rows == 1:
+        pitch = cols
+    elif pitch < cols:
+        raise ValueError(f"the rows of {name} overlap in memory")
+    return rows, cols, pitch
+
+
+def _vector(t, name, n, device):
+    """Pointer and type of an n-element parameter vector (None: absent)."""
+    if t is None:
+        return None
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, x on {device}: all operands must be on one device")
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be {n} contiguous elements")
+    return t.data_ptr()
+
+
+def _span(t, rows, cols, pitch):
+    first = t.data_ptr()
+    return first, first + ((rows - 1) * pitch + cols) * t.element_size()
+
+
+def _refuse_overlap(out, out_rows, t, t_rows, name, what):
+    """An output may be an input itself, row on row, but not overlap it otherwise."""
+    if out_rows[0] == 0:
+        return
+    a, b = _span(out, *out_rows), _span(t, *t_rows)
+    if a[0] < b[1] and b[0] < a[1] and not (a[0] == b[0] and out_rows == t_rows and out.dtype == t.dtype):
+        raise ValueError(f"{what} overlaps {name} in memory; it may only be {name} itself")
+
+
+def _enter(device, stream):
+    """The launch stream's handle, and whether it is another than the
+    device's current one (whose allocator order then has to be kept)."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError("operands must be CUDA tensors")
+    cur = torch.cuda.current_stream(device)
+    if stream is None:
+        return cur.cuda_stream, None
+    if getattr(stream, "device", device) != device:
+        raise ValueError(f"stream belongs to {stream.device}, operands to {device}")
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle == cur.cuda_stream:
+        return handle, None
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(handle, device=device)
+    # What this call allocates may reuse memory that work on the current
+    # stream still touches.
+    stream.wait_stream(cur)
+    return handle, stream
+
+
+def _record(other, *tensors):
+    """Memory used on a stream that is not the current one is not handed out
+    again before that stream has passed this point."""
+    if other is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(other)
+
+
+def _on(device):
+    """The context in which the library is called: `device` current."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _workspace(kind, device, handle, nbytes, other):
+    """A buffer kept per operator, device and stream, grown as needed: calls
+    on one stream never overlap."""
+    import torch
+    key = (kind, device.index, handle)
+    buf = _workspaces.get(key)
+    if buf is None or buf.numel() < nbytes:
+        buf = _workspaces[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _record(other, buf)
+    return buf
+
+
+def layer_norm(x, weight=None, bias=None, out=None, *, eps=1e-5, stats=False, stream=None):
+    """Layer norm over the last dimension of x (float32 or bfloat16).
+
+    y = (x - mean) * rstd * weight + bias in float32, rounded once to x's
+    type; rstd = 1 / sqrt(var + eps) with the biased variance.  weight and
+    bias (each optional) are float32 or bfloat16 vectors, both of one type.
+    Rows may lie at any common distance (a column slice of a wider buffer).
+    out: where y goes (x itself for an in-place call); allocated if None.
+
+    stats: return (y, mean, rstd) with the rows' float32 statistics, which
+    layer_norm_backward takes; otherwise y alone."""
+    import torch
+    dt = _dtype(x, "x")
+    rows = _rows(x, "x")
+    device = x.device
+    handle, other = _enter(device, stream)
+    pw, pb = _vector(weight, "weight", rows[1], device), _vector(bias, "bias", rows[1], device)
+    wdt = F32
+    if weight is not None:
+        wdt = _dtype(weight, "weight")
+        if bias is not None and bias.dtype != weight.dtype:
+            raise TypeError("weight and bias must have one type")
+    elif bias is not None:
+        wdt = _dtype(bias, "bias")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=device)
+        out_rows = (rows[0], rows[1], rows[1])
+    else:
+        if out.device != device:
+            raise ValueError(f"out is on {out.device}, x on {device}: all operands must be on one device")
+        if out.shape != x.shape or out.dtype != x.dtype:
+            raise ValueError("out must have x's shape and type")
+        out_rows = _rows(out, "out")
+        _refuse_overlap(out, out_rows, x, rows, "x", "out")
+    mean = rstd = None
+    if stats:
+        both = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=device)
+        mean, rstd = both[0], both[1]
+    with _on(device):
+        st = _pg.lib().layer_norm(rows[0], rows[1], x.data_ptr(), rows[2], dt, pw, pb, wdt, out.data_ptr(),
+                                  out_rows[2], mean.data_ptr() if stats else None, rstd.data_ptr() if stats else None,
+                                  eps, handle)
+    _pg._check(st, "layer_norm")
+    _record(other, x, weight, bias, out, mean)
+    return (out, mean, rstd) if stats else out
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, *, stream=None):
+    """(dx, dweight, dbias) of layer_norm from dy, its input x, the mean and
+    rstd it returned, and its weight.
+
+    dx has x's type; dweight and dbias have weight's type and are None when
+    weight is None.  All sums are float32 in an order fixed by the sizes: the
+    same inputs give the same bits.  out: where dx goes (dy or x itself for an
+    in-place call); allocated if None."""
+    import torch
+    dt = _dtype(x, "x")
+    rows = _rows(x, "x")
+    device = x.device
+    handle, other = _enter(device, stream)
+    if dy.device != device:
+        raise ValueError(f"dy is on {dy.device}, x on {device}: all operands must be on one device")
+    if dy.shape != x.shape or dy.dtype != x.dtype:
+        raise ValueError("dy must have x's shape and type")
+    dy_rows = _rows(dy, "dy")
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, x on {device}: all operands must be on one device")
+        if t.dtype != torch.float32 or t.numel() != rows[0] or not t.is_contiguous():
+            raise ValueError(f"{name} must be {rows[0]} contiguous float32 values")
+    pw = _vector(weight, "weight", rows[1], device)
+    wdt = F32
+    dweight = dbias = ws = None
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=device)
+        out_rows = (rows[0], rows[1], rows[1])
+    else:
+        if out.device != device:
+            raise ValueError(f"out is on {out.device}, x on {device}: all operands must be on one device")
+        if out.shape != x.shape or out.dtype != x.dtype:
+            raise ValueError("out must have x's shape and type")
+        out_rows = _rows(out, "out")
+        _refuse_overlap(out, out_rows, x, rows, "x", "out")
+        _refuse_overlap(out, out_rows, dy, dy_rows, "dy", "out")
+    l = _pg.lib()
+    with _on(device):
+        if weight is not None:
+            wdt = _dtype(weight, "weight")
+            both = torch.empty((2, rows[1]), dtype=weight.dtype, device=device)
+            dweight, dbias = both[0], both[1]
+            need = ctypes.c_size_t()
+            _pg._check(l.layer_norm_backward_workspace(rows[0], rows[1], ctypes.byref(need)),
+                       "layer_norm_backward_workspace")
+            ws = _workspace("layer_norm_backward", device, handle, need.value, other)
+        st = l.layer_norm_backward(rows[0], rows[1], dy.data_ptr(), dy_rows[2], x.data_ptr(), rows[2], dt,
+                                   mean.data_ptr(), rstd.data_ptr(), pw, wdt, out.data_ptr(), out_rows[2],
+                                   dweight.data_ptr() if ws is not None else None,
+                                   dbias.data_ptr() if ws is not None else None,
+                                   ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+                                   handle)
+    _pg._check(st, "layer_norm_backward")
+    _record(other, dy, x, mean, rstd, weight, out, dweight)
+    return out, dweight, dbias

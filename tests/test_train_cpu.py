@@ -1,0 +1,67 @@
+"""The training operators' checks that need no GPU: the C ABI's argument
+validation (made before any device is asked) and the binding's refusals."""
+import ctypes
+
+import pytest
+
+import async_copy_pipelined_gb300 as pg
+
+INVALID, MISALIGNED = 1, 2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    pg.build()
+    return pg.lib()
+
+
+def _forward(lib, rows=4, cols=8, x=256, ldx=8, dtype=0, w=256, b=256, wdtype=0, y=512, ldy=8, mean=1024, rstd=2048,
+             eps=1e-5):
+    return lib.layer_norm(rows, cols, x, ldx, dtype, w, b, wdtype, y, ldy, mean, rstd, eps, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(rows=-1), INVALID), (dict(cols=0), INVALID), (dict(dtype=2), INVALID), (dict(wdtype=-1), INVALID),
+    (dict(ldx=7), INVALID), (dict(ldy=7), INVALID), (dict(x=None), INVALID), (dict(y=None), INVALID),
+    (dict(mean=None), INVALID), (dict(eps=-1e-5), INVALID), (dict(eps=float("nan")), INVALID),
+    (dict(eps=float("inf")), INVALID), (dict(x=258), MISALIGNED), (dict(w=257, wdtype=1), MISALIGNED),
+    (dict(y=513, dtype=1), MISALIGNED), (dict(mean=1026), MISALIGNED),
+])
+def test_layer_norm_validation(lib, kw, status):
+    assert _forward(lib, **kw) == status
+
+
+def _backward(lib, rows=4, cols=8, dy=256, lddy=8, x=256, ldx=8, dtype=0, mean=1024, rstd=2048, w=256, wdtype=0, dx=512,
+              lddx=8, dw=4096, db=8192, ws=16384, ws_bytes=1 << 20):
+    return lib.layer_norm_backward(rows, cols, dy, lddy, x, ldx, dtype, mean, rstd, w, wdtype, dx, lddx, dw, db, ws,
+                                   ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(rows=-1), INVALID), (dict(cols=0), INVALID), (dict(dtype=3), INVALID), (dict(lddy=7), INVALID),
+    (dict(lddx=7), INVALID), (dict(mean=None), INVALID), (dict(dx=None), INVALID), (dict(ws=None), INVALID),
+    (dict(ws_bytes=255), INVALID), (dict(ws=16392), MISALIGNED), (dict(dx=514), MISALIGNED),
+    (dict(dw=4097, wdtype=1), MISALIGNED),
+])
+def test_layer_norm_backward_validation(lib, kw, status):
+    assert _backward(lib, **kw) == status
+
+
+def test_layer_norm_backward_workspace(lib):
+    n = ctypes.c_size_t()
+    assert lib.layer_norm_backward_workspace(4, 8, ctypes.byref(n)) == 0
+    assert n.value >= 4 * 2 * 8 * 4
+    assert lib.layer_norm_backward_workspace(-1, 8, ctypes.byref(n)) == INVALID
+    assert lib.layer_norm_backward_workspace(4, 0, ctypes.byref(n)) == INVALID
+    assert lib.layer_norm_backward_workspace(4, 8, None) == INVALID
+
+
+def test_host_tensors_are_refused(lib):
+    import torch
+    x = torch.ones((4, 8))
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        pg.layer_norm(x)
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        pg.layer_norm_backward(x, x, torch.ones(4), torch.ones(4))
+    with pytest.raises(TypeError):
+        pg.layer_norm(x.double())
