@@ -22,7 +22,7 @@ import threading
 __all__ = [
     "FILL", "OPTIONS", "GemmError", "lib", "library_path", "gemm_f32", "gemm_bf16", "plan_f32", "plan_bf16",
     "device_status", "selftest_bounded_wait", "testing_set_hooks", "status_string", "build",
-    "layer_norm", "layer_norm_backward",
+    "layer_norm", "layer_norm_backward", "orthogonalize",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -572,4 +572,4 @@ def f32_wide_rows(M: int, N: int, K: int, sms: int = 152, mode: int = -1) -> int
     return r
 
 
-from .training import layer_norm, layer_norm_backward  # noqa: E402  (training calls back into this module)
+from .training import layer_norm, layer_norm_backward, orthogonalize  # noqa: E402  (training calls back into this module)

@@ -137,6 +137,18 @@ unsigned int *device_status_word(int dev, unsigned long long ctx);
 int encode_tensor_map_2d(void *map_out, int dtype_is_bf16, const void *base, uint64_t cols, uint64_t rows,
                          uint64_t pitch_bytes, uint32_t box_cols, uint32_t box_rows, int swizzle_128b);
 
+// A 3-D tiled tensor map over 2-byte floating elements (float16 or bfloat16:
+// the copies move bits, and an element outside is zero in both) or float32
+// ones: `planes` matrices of rows x cols, pitches in bytes.
+enum TensorElement { kElement16, kElement32 };
+int encode_tensor_map_3d(void *map_out, TensorElement element, const void *base, uint64_t cols, uint64_t rows,
+                         uint64_t planes, uint64_t row_pitch, uint64_t plane_pitch, uint32_t box_cols,
+                         uint32_t box_rows, bool swizzle_128b);
+
+// This call's wait limit and withheld ring position (test hooks included).
+unsigned long long call_wait_limit_ns();
+int call_withhold();
+
 // Status codes recorded on device: low byte = kernel family, next byte = role.
 constexpr unsigned int kErrFamilyF32Tma = 1;
 constexpr unsigned int kErrFamilyBf16 = 2;
@@ -144,6 +156,7 @@ constexpr unsigned int kErrFamilySelftest = 3;
 constexpr unsigned int kErrFamilyF32CpAsyncMbar = 4;
 constexpr unsigned int kErrFamilyF32CpAsyncWs = 5;
 constexpr unsigned int kErrFamilyF32TmaWide = 6;
+constexpr unsigned int kErrFamilyOrthogonalize = 7;
 constexpr unsigned int kErrRoleConsumer = 1u << 8;
 constexpr unsigned int kErrRoleProducer = 2u << 8;
 constexpr unsigned int kErrRoleMma = 3u << 8;

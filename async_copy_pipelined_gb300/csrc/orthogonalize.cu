@@ -1,0 +1,1237 @@
+// Newton-Schulz orthogonalisation of a weight's update.
+//
+//   X <- G / (|G|_F + eps), transposed where G is tall, so X is r x c, r <= c
+//   steps times:  A = X X^T,   Q = a I + b A + c A A,   X <- Q X
+//
+// The three products are nearly all of the work: r r c multiply-adds for Q X
+// and, A and A A being symmetric, half of r r c and of r r r for the others
+// (one triangle of tiles is computed, its mirror image stored).  All of them
+// run on one tcgen05 kernel (the TMA ring of the BF16 GEMM) with float16
+// operands and float32 accumulators.
+//
+// Precision.  One float16 operand has 11 significant bits, and what rounding
+// an iterate loses does not stay small: the iteration multiplies a singular
+// direction far below the largest by a = 3.4 per step, the rounding errors
+// that fall on it included.  So each matrix is kept as a sum of float16
+// planes, x = x0 + x1 (+ x2), each plane the rounding of what the planes
+// before it left over, and a product runs over pairs of planes, all into one
+// accumulator.  Which pairs are needed differs by matrix:
+//
+//   X     Every bit lost in X is lost in its small singular directions, so X
+//         carries one plane more than the result's type asks for.
+//   A, Q  An error in an entry of A or Q acts on X from the left, spread over
+//         the row; only the diagonal, large beside the rest in the late
+//         steps, needs the extra plane.  It is kept and multiplied for the
+//         256 x 256 blocks on the diagonal alone.
+//
+//   bfloat16 result:  A one pair, A A one, Q X two (one in the last step,
+//                     whose roundings no later step multiplies).
+//   float32 result:   A three pairs, A A three, Q X five (three in the last).
+//
+// Measured in float64 arithmetic on spectra from flat to 1e-3 of the largest
+// value (256 .. 1000 rows): the bfloat16 result is off by 1.03 to 1.15 times
+// the error of rounding the exact result; one pair throughout by up to 16
+// times.
+//
+// A A is never added to b A: the square is completed,
+//   Q = c (A + (b / 2c) I)^2 + (a - b b / 4c) I,
+// so that the kernel's whole epilogue is a scaling and a diagonal, and reads
+// nothing.  (c = 0: Q = a I + b A straight from X X^T.)
+//
+// Scaling.  G is multiplied by a power of two only, which keeps bfloat16
+// entries exact in float16; the rest of 1 / (|G|_F + eps), a factor f in
+// [1, 2), goes into the first step's epilogues in float32.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include <cuda_fp16.h>
+
+#include "gemm_internal.h"
+#include "pipelined_train.h"
+#include "ptx.cuh"
+#include "tma_ring.cuh"
+#include "vector_io.cuh"
+
+namespace pg {
+
+namespace orth {
+
+constexpr int BK = 64;                          // K block: 128 bytes of float16
+constexpr int kUmmaM = 128;
+constexpr int kUmmaK = 16;
+constexpr int kBox = 64;                        // every load is a 64 x 64 box
+constexpr uint32_t kBoxBytes = kBox * kBox * 2; // 8 KiB
+constexpr int kDiagBlock = 256;                 // side of the diagonal blocks that keep the extra plane
+constexpr uint32_t kStagingBytes = 32 * 128;    // per epilogue warp: 32 rows of 128 bytes
+
+// Powers of two the planes are scaled by: the largest magnitudes they must
+// hold under float16's 65504 are X 4, A + (b / 2c) I 8, Q 32 (orthogonalize()
+// refuses coefficients that reach further), and nothing that matters at the
+// other end falls below its 2^-14.
+constexpr float kScaleX = 16384.0f, kScaleA = 8192.0f, kScaleQ = 2048.0f;
+
+// One pair of planes to multiply.  Plane -1 is the diagonal-block plane.
+// `range`: all of K, or the K of this tile's rows or columns.
+enum Range { kAll, kRows, kCols };
+struct Pass {
+    signed char left, right, range;
+};
+constexpr int kMaxPasses = 6;
+
+// The tensor cores add to a float32 accumulator by truncation: n additions in
+// a row lose about n 2^-25 of a sum of equal signs (A's diagonal), which a
+// bfloat16 result does not notice and a float32 one does.  There (Product.fine)
+// each K block (four additions) of the one pass over the leading planes has an
+// accumulator of its own, and the epilogue adds them with rounding; the other
+// passes' terms are 2^-11 as large and share one.  Error of the float32 result
+// against float64, 1000 x 3000, flat and decaying spectrum: 9.5e-6 and 1.2e-5
+// with four K blocks to an accumulator, 3.1e-6 and 4.2e-6 with one; the same
+// products in float32 arithmetic give 3.7e-6 and 7.0e-6.
+
+enum Output { kPlanes, kBf16, kF32 };
+
+struct Maps {
+    CUtensorMap left, left_diag, right, right_diag; // 64 x 64 boxes, 128-byte swizzle
+    CUtensorMap store, mirror, store_diag, mirror_diag;
+};
+
+// D (rows x cols, a batch of them) = sum over the passes of left plane times
+// right plane over k, scaled by alpha, plus diag on the diagonal.
+struct Product {
+    int rows, cols, k, batch;
+    int symmetric; // compute the tiles on and above the diagonal, store both
+    int left_planes, right_planes;
+    int passes;
+    Pass pass[kMaxPasses];
+    int fine; // an accumulator for each K block of the last pass, one for the passes before it
+    float alpha, diag;
+    int alpha_power, diag_power; // of f
+    const float *f;              // one per matrix
+    int output;                  // Output
+    int planes;                  // kPlanes: how many to write
+    int planes_pitch;            // kPlanes: planes per matrix of the batch
+    int diag_plane;              // kPlanes: also one more on the diagonal blocks
+    int transposed;              // final output: D^T
+    int out_tma;                 // final output through TMA stores
+    void *out;
+    long long ldo, out_batch;    // elements
+    unsigned int *status;
+    unsigned long long wait_limit_ns;
+    int withhold;
+};
+
+// Tile of MH x 128 rows by BN columns, S ring stages.  The 256 x 256 tile
+// fills tensor memory with one accumulator and has each of its eight epilogue
+// warps take a quarter's 256 columns in turn; the 128 x 128 tile has four
+// accumulators and each warp takes 64 columns at once, so that it can also
+// sum a tile's accumulators in registers (Product.fine).
+template <int MH, int BN, int S>
+struct Tile {
+    static constexpr int BM = kUmmaM * MH;
+    static constexpr uint32_t kLeftBytes = BM * BK * 2;
+    static constexpr uint32_t kStageBytes = kLeftBytes + BN * BK * 2;
+    static constexpr int kAccBufs = 512 / (MH * BN);
+    static constexpr uint32_t kTmemCols = 512;
+    static constexpr int kEpiWarps = 8;
+    static constexpr int kEpiCols = MH * BN / 2; // columns per epilogue warp
+    static constexpr int kThreads = (2 + kEpiWarps) * 32;
+    static constexpr int kSmem = S * kStageBytes + kEpiWarps * kStagingBytes + 1024 /* barriers */ + 1024 /* slack */;
+    static_assert(MH * BN <= 512 && kEpiCols % 64 == 0, "accumulators fit tensor memory");
+};
+
+// Tile t of the batch: matrix b, tile row i, tile column j.  The upper
+// triangle goes column by column; a full matrix in groups of 16 tile rows.
+struct TileAt {
+    int b, i, j;
+};
+
+__host__ __device__ inline int tiles_of(bool symmetric, int tiles_m, int tiles_n)
+{
+    return symmetric ? tiles_m * (tiles_m + 1) / 2 : tiles_m * tiles_n;
+}
+
+__device__ __forceinline__ TileAt tile_at(int t, bool symmetric, int tiles_m, int tiles_n)
+{
+    const int per = tiles_of(symmetric, tiles_m, tiles_n);
+    TileAt at;
+    at.b = t / per;
+    int r = t - at.b * per;
+    if (symmetric) {
+        int j = static_cast<int>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
+        while (j * (j + 1) / 2 > r)
+            --j;
+        while ((j + 1) * (j + 2) / 2 <= r)
+            ++j;
+        at.j = j;
+        at.i = r - j * (j + 1) / 2;
+    } else {
+        constexpr int kGroup = 16;
+        const int group = r / (kGroup * tiles_n);
+        const int first = group * kGroup;
+        const int gm = min(kGroup, tiles_m - first);
+        r -= group * kGroup * tiles_n;
+        at.i = first + r % gm;
+        at.j = r / gm;
+    }
+    return at;
+}
+
+// K blocks of one pass for a tile whose rows start at row0 and columns at col0.
+template <int BM, int BN>
+__device__ __forceinline__ void pass_range(const Pass &pass, int k, int row0, int col0, int &k0, int &blocks)
+{
+    k0 = pass.range == kAll ? 0 : pass.range == kRows ? row0 : col0;
+    const int k1 = pass.range == kAll ? k : min(k, k0 + (pass.range == kRows ? BM : BN));
+    blocks = (k1 - k0 + BK - 1) / BK;
+}
+
+// K blocks of one tile: of all its passes but the last, and of all.
+struct Blocks {
+    int before, all;
+    // Whether an accumulator ends with block kb, and how many there are.
+    __device__ __forceinline__ bool ends(int kb, bool fine) const { return kb == all - 1 || (fine && kb >= before - 1); }
+    __device__ __forceinline__ int accumulators(bool fine) const
+    {
+        return fine ? (before > 0 ? 1 : 0) + all - before : 1;
+    }
+};
+
+template <int BM, int BN>
+__device__ __forceinline__ Blocks tile_blocks(const Product &p, const TileAt &at)
+{
+    Blocks n{0, 0};
+    for (int ps = 0; ps < p.passes; ++ps) {
+        int k0, blocks;
+        pass_range<BM, BN>(p.pass[ps], p.k, at.i * BM, at.j * BN, k0, blocks);
+        n.before = n.all;
+        n.all += blocks;
+    }
+    return n;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float2 unpack_f16(uint32_t w)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// One epilogue warp's 4 KiB staging buffer, from which a TMA store moves a
+// box.  Each write waits until the store before it has read the buffer.
+struct Staging {
+    uint32_t addr;
+    int lane;
+
+    __device__ __forceinline__ void begin() const
+    {
+        if (lane == 0)
+            bulk_wait_group_read<0>();
+        __syncwarp();
+    }
+    __device__ __forceinline__ void end(const CUtensorMap *map, int x, int y, int z) const
+    {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(map, addr, x, y, z);
+            bulk_commit_group();
+        }
+    }
+    // 32 words of this lane's row, in the 128-byte swizzle.
+    __device__ __forceinline__ void row(const uint32_t (&w)[32]) const
+    {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(
+                             addr + static_cast<uint32_t>(lane * 128 + ((j ^ (lane & 7)) << 4))),
+                         "r"(w[4 * j]), "r"(w[4 * j + 1]), "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
+                         : "memory");
+    }
+    // The transpose: 64 rows of 32 two-byte elements, this lane's column.
+    __device__ __forceinline__ void column16(const uint32_t (&w)[32]) const
+    {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const uint32_t at = addr + static_cast<uint32_t>(j * 128 + lane * 2);
+            asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at), "h"(static_cast<uint16_t>(w[j] & 0xFFFFu)) : "memory");
+            asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at + 64u), "h"(static_cast<uint16_t>(w[j] >> 16))
+                         : "memory");
+        }
+    }
+    // 32 rows of 32 four-byte elements, this lane's column.
+    __device__ __forceinline__ void column32(const uint32_t (&w)[32]) const
+    {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(addr + static_cast<uint32_t>(j * 128 + lane * 4)), "r"(w[j])
+                         : "memory");
+    }
+};
+
+// RightMN: the right operand's rows are k (Q X); otherwise its rows are D's
+// columns (X X^T, and the symmetric A A).
+template <int MH, int BN, int S, bool RightMN>
+__global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
+    product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Product p)
+{
+    using T = Tile<MH, BN, S>;
+    constexpr int BM = T::BM;
+    // Instruction descriptor, kind::f16: D float32 (bits 4-5 = 1), A and B
+    // float16 (bits 7-12 = 0), A K-major, B K-major or MN-major (bit 16),
+    // N >> 3 at bits 17-22, M >> 4 at bits 24-28.
+    constexpr uint32_t kIdesc = (1u << 4) | (RightMN ? 1u << 16 : 0u) | (static_cast<uint32_t>(BN >> 3) << 17) |
+                                (static_cast<uint32_t>(kUmmaM >> 4) << 24);
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = align_smem(raw, 1024);
+    const uint32_t staging0 = base + S * T::kStageBytes;
+    const uint32_t bars = staging0 + T::kEpiWarps * kStagingBytes;
+    const TmaRing<S> ring{bars, bars + 8u * S};
+    const uint32_t tmem_full0 = bars + 16u * S;                  // [kAccBufs]
+    const uint32_t tmem_empty0 = tmem_full0 + 8u * T::kAccBufs; // [kAccBufs]
+    const uint32_t epi_done = tmem_empty0 + 8u * T::kAccBufs;
+    const uint32_t mma_done = epi_done + 8u;
+    const uint32_t tmem_slot = mma_done + 8u;
+    volatile uint32_t *tmem_slot_ptr = reinterpret_cast<volatile uint32_t *>(smem_raw + (tmem_slot - raw));
+
+    const int warp = threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    const bool symmetric = p.symmetric != 0;
+    const int tiles_m = (p.rows + BM - 1) / BM;
+    const int tiles_n = (p.cols + BN - 1) / BN;
+    const int num_tiles = tiles_of(symmetric, tiles_m, tiles_n) * p.batch;
+
+    if (threadIdx.x == 0) {
+        ring.init(1);
+        for (int b = 0; b < T::kAccBufs; ++b) {
+            mbar_init(tmem_full0 + 8u * b, 1);
+            mbar_init(tmem_empty0 + 8u * b, T::kEpiWarps);
+        }
+        mbar_init(epi_done, T::kEpiWarps);
+        mbar_init(mma_done, 1);
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, T::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot_ptr;
+    grid_launch_next();
+    grid_wait(); // the operands, f, and the buffers this product overwrites
+
+    if (warp == 0) {
+        // ------------------------------------------------------- TMA producer
+        if (lane == 0) {
+            int f = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+                const TileAt at = tile_at(t, symmetric, tiles_m, tiles_n);
+                const int row0 = at.i * BM, col0 = at.j * BN;
+                for (int ps = 0; ps < p.passes && ok; ++ps) {
+                    const Pass pass = p.pass[ps];
+                    int k0, blocks;
+                    pass_range<BM, BN>(pass, p.k, row0, col0, k0, blocks);
+                    const bool ld = pass.left < 0, rd = pass.right < 0;
+                    const CUtensorMap *lmap = ld ? &maps.left_diag : &maps.left;
+                    const CUtensorMap *rmap = rd ? &maps.right_diag : &maps.right;
+                    const int lz = ld ? at.b : at.b * p.left_planes + pass.left;
+                    const int rz = rd ? at.b : at.b * p.right_planes + pass.right;
+                    for (int kb = 0; kb < blocks; ++kb, ++f) {
+                        if (f == p.withhold)
+                            continue; // test hook: this position is never filled
+                        if (!ring.producer_acquire(f, p.wait_limit_ns)) {
+                            record_error(p.status, kErrFamilyOrthogonalize | kErrRoleProducer);
+                            ok = false;
+                            break;
+                        }
+                        const int k = k0 + kb * BK;
+                        const int lx = ld ? k % kDiagBlock : k, rx = rd ? k % kDiagBlock : k;
+                        const uint32_t dst = base + static_cast<uint32_t>(f % S) * T::kStageBytes;
+                        const uint32_t full = ring.full_bar(f);
+                        ring.producer_commit(f, T::kStageBytes);
+#pragma unroll
+                        for (int q = 0; q < BM / kBox; ++q)
+                            tma_load_3d(dst + q * kBoxBytes, lmap, full, lx, row0 + q * kBox, lz);
+#pragma unroll
+                        for (int q = 0; q < BN / kBox; ++q) {
+                            const uint32_t to = dst + T::kLeftBytes + q * kBoxBytes;
+                            if constexpr (RightMN)
+                                tma_load_3d(to, rmap, full, col0 + q * kBox, k, rz);
+                            else
+                                tma_load_3d(to, rmap, full, rx, col0 + q * kBox, rz);
+                        }
+                    }
+                }
+            }
+            // Only the last S positions issued can still be in flight.
+            bool drained = true;
+            for (int g = f > S ? f - S : 0; g < f; ++g)
+                if (g != p.withhold && !ring.consumer_wait(g, p.wait_limit_ns))
+                    drained = false;
+            if (!drained)
+                record_error(p.status, kErrFamilyOrthogonalize | kErrRoleDrain);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            int f = 0;
+            bool ok = true;
+            int acc = 0; // accumulators begun
+            for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+                const TileAt at = tile_at(t, symmetric, tiles_m, tiles_n);
+                const Blocks blocks = tile_blocks<BM, BN>(p, at);
+                uint32_t d_tmem = tmem_base, full_bar = tmem_full0;
+                bool fresh = true; // the next block begins an accumulator
+                for (int kb = 0; kb < blocks.all; ++kb, ++f) {
+                    if (fresh) {
+                        const int slot = acc % T::kAccBufs;
+                        const uint32_t use_parity = static_cast<uint32_t>((acc / T::kAccBufs) & 1);
+                        if (!mbar_wait_bounded(tmem_empty0 + 8u * slot, use_parity ^ 1u, p.wait_limit_ns)) {
+                            record_error(p.status, kErrFamilyOrthogonalize | kErrRoleMma);
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                        d_tmem = tmem_base + static_cast<uint32_t>(slot * MH * BN);
+                        full_bar = tmem_full0 + 8u * slot;
+                        ++acc;
+                    }
+                    if (!ring.consumer_wait(f, p.wait_limit_ns)) {
+                        record_error(p.status, kErrFamilyOrthogonalize | kErrRoleMma);
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t a_addr = base + static_cast<uint32_t>(f % S) * T::kStageBytes;
+                    const uint32_t b_addr = a_addr + T::kLeftBytes;
+#pragma unroll
+                    for (int ks = 0; ks < BK / kUmmaK; ++ks) {
+                        // K step: 32 bytes along a K-major row; 16 rows of 128
+                        // bytes of an MN-major box.
+                        const uint64_t bdesc =
+                            RightMN ? smem_desc_sw128(b_addr + ks * kUmmaK * 128, kBoxBytes, 1024)
+                                    : smem_desc_sw128(b_addr + ks * kUmmaK * 2, 16, 1024);
+#pragma unroll
+                        for (int h = 0; h < MH; ++h) {
+                            const uint64_t adesc =
+                                smem_desc_sw128(a_addr + h * (kUmmaM * 128) + ks * kUmmaK * 2, 16, 1024);
+                            mma_f16_ss(d_tmem + static_cast<uint32_t>(h * BN), adesc, bdesc, kIdesc,
+                                       (!fresh || ks != 0) ? 1u : 0u);
+                        }
+                    }
+                    mma_commit(ring.empty_bar(f)); // stage free once these MMAs have read it
+                    fresh = blocks.ends(kb, p.fine != 0);
+                    if (fresh)
+                        mma_commit(full_bar); // accumulator complete
+                }
+            }
+            // Every MMA this thread issued must finish before tensor memory is freed.
+            mma_commit(mma_done);
+            if (!mbar_wait_bounded(mma_done, 0, p.wait_limit_ns))
+                record_error(p.status, kErrFamilyOrthogonalize | kErrRoleDrain);
+        }
+        __syncwarp();
+        if (!mbar_wait_bounded(epi_done, 0, p.wait_limit_ns) && lane == 0)
+            record_error(p.status, kErrFamilyOrthogonalize | kErrRoleDrain);
+        tc_fence_after_sync();
+        __syncwarp();
+        tmem_dealloc(tmem_base, T::kTmemCols);
+    } else {
+        // ------------------------------------------------------- epilogue
+        const int quarter = warp & 3; // the tensor-memory lanes this warp may read
+        const int epi = warp - 2;
+        const int half = MH == 2 ? epi / 4 : 0;                      // of the tile's rows
+        const int first_col = MH == 2 ? 0 : (epi / 4) * T::kEpiCols; // of the tile's columns
+        const Staging staging{staging0 + static_cast<uint32_t>(epi) * kStagingBytes, lane};
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        int acc = 0; // accumulators taken
+        for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
+            const TileAt at = tile_at(t, symmetric, tiles_m, tiles_n);
+            const float f = p.f[at.b];
+            float alpha = p.alpha, diag = p.diag;
+            for (int e = 0; e < p.alpha_power; ++e)
+                alpha *= f;
+            for (int e = 0; e < p.diag_power; ++e)
+                diag *= f;
+            const int row0 = at.i * BM + half * kUmmaM + quarter * 32;
+            const int row = row0 + lane;
+            const bool mirrored = symmetric && at.i != at.j;
+
+            // 64 columns of a finished accumulator, added to v.
+            auto take = [&](int slot, int column, float (&v)[64]) {
+                uint32_t r0[32], r1[32];
+                const uint32_t taddr = tmem_base + lanes + static_cast<uint32_t>((slot * MH + half) * BN + column);
+                tmem_ld_32x32b_x32(taddr, r0);
+                tmem_ld_32x32b_x32(taddr + 32u, r1);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    v[j] += __uint_as_float(r0[j]);
+                    v[32 + j] += __uint_as_float(r1[j]);
+                }
+            };
+            // Wait for accumulator `acc`; false when the wait ran out.
+            auto wait_full = [&]() {
+                const bool ok = mbar_wait_bounded(tmem_full0 + 8u * (acc % T::kAccBufs),
+                                                  static_cast<uint32_t>((acc / T::kAccBufs) & 1), p.wait_limit_ns);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    if (lane == 0)
+                        record_error(p.status, kErrFamilyOrthogonalize | kErrRoleEpilogue);
+                    return false;
+                }
+                tc_fence_after_sync();
+                return true;
+            };
+            // The accumulator has been read (tcgen05.wait::ld): hand it back.
+            auto release = [&]() {
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(tmem_empty0 + 8u * (acc % T::kAccBufs));
+                ++acc;
+            };
+            // 64 columns of this warp's 32 rows, scaled and stored.
+            auto emit = [&](float (&v)[64], int col0) {
+#pragma unroll
+                for (int j = 0; j < 64; ++j)
+                    v[j] *= alpha;
+                if (p.diag != 0.0f && row0 < col0 + 64 && col0 < row0 + 32) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j)
+                        if (col0 + j == row)
+                            v[j] += diag;
+                }
+                uint32_t w[32];
+                if (p.output == kPlanes) {
+                    const bool on_diag = p.diag_plane != 0 && row0 / kDiagBlock == col0 / kDiagBlock;
+                    const int planes = p.planes + (on_diag ? 1 : 0);
+#pragma unroll 1
+                    for (int q = 0; q < planes; ++q) {
+                        const bool extra = q == p.planes;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            w[j] = pack_f16(v[2 * j], v[2 * j + 1]);
+                            const float2 kept = unpack_f16(w[j]);
+                            v[2 * j] -= kept.x; // exact: what this plane leaves over
+                            v[2 * j + 1] -= kept.y;
+                        }
+                        staging.begin();
+                        staging.row(w);
+                        if (extra)
+                            staging.end(&maps.store_diag, col0 % kDiagBlock, row0, at.b);
+                        else
+                            staging.end(&maps.store, col0, row0, at.b * p.planes_pitch + q);
+                        if (mirrored) {
+                            staging.begin();
+                            staging.column16(w);
+                            if (extra)
+                                staging.end(&maps.mirror_diag, row0 % kDiagBlock, col0, at.b);
+                            else
+                                staging.end(&maps.mirror, row0, col0, at.b * p.planes_pitch + q);
+                        }
+                    }
+                } else if (p.out_tma && p.output == kBf16) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+                    staging.begin();
+                    if (p.transposed) {
+                        staging.column16(w);
+                        staging.end(&maps.store, row0, col0, at.b);
+                    } else {
+                        staging.row(w);
+                        staging.end(&maps.store, col0, row0, at.b);
+                    }
+                } else if (p.out_tma) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (col0 + 32 * h >= p.cols)
+                            break; // warp-uniform
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            w[j] = __float_as_uint(v[32 * h + j]);
+                        staging.begin();
+                        if (p.transposed) {
+                            staging.column32(w);
+                            staging.end(&maps.store, row0, col0 + 32 * h, at.b);
+                        } else {
+                            staging.row(w);
+                            staging.end(&maps.store, col0 + 32 * h, row0, at.b);
+                        }
+                    }
+                } else if (row < p.rows) {
+                    // Rows that TMA cannot store (not 16-byte aligned): one
+                    // guarded element each.
+                    const long long first = at.b * p.out_batch;
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) {
+                        if (col0 + j < p.cols) {
+                            const long long o = first + (p.transposed ? (col0 + j) * p.ldo + row
+                                                                      : row * p.ldo + col0 + j);
+                            store_f32(p.out, p.output == kBf16, o, v[j]);
+                        }
+                    }
+                }
+            };
+
+            if constexpr (T::kEpiCols == 64) {
+                const int parts = tile_blocks<BM, BN>(p, at).accumulators(p.fine != 0);
+                float v[64];
+#pragma unroll
+                for (int j = 0; j < 64; ++j)
+                    v[j] = 0.0f;
+                bool ok = true;
+                for (int part = 0; part < parts && ok; ++part) {
+                    ok = wait_full();
+                    if (ok) {
+                        take(acc % T::kAccBufs, first_col, v);
+                        release();
+                    }
+                }
+                if (!ok)
+                    break;
+                const int col0 = at.j * BN + first_col;
+                if (row0 < p.rows && col0 < p.cols) // warp-uniform
+                    emit(v, col0);
+            } else {
+                if (!wait_full())
+                    break;
+#pragma unroll 1
+                for (int c = 0; c < T::kEpiCols; c += 64) {
+                    const int col0 = at.j * BN + first_col + c;
+                    if (col0 >= p.cols || row0 >= p.rows)
+                        break; // warp-uniform: nothing of this box lies in the matrix
+                    float v[64];
+#pragma unroll
+                    for (int j = 0; j < 64; ++j)
+                        v[j] = 0.0f;
+                    take(acc % T::kAccBufs, first_col + c, v);
+                    emit(v, col0);
+                }
+                release();
+            }
+        }
+        if (lane == 0)
+            bulk_wait_group<0>(); // every store of this warp is done
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(epi_done);
+    }
+}
+
+// ------------------------------------------------------------ norm and planes of G
+struct Input {
+    const void *G;
+    int bf16;
+    int m, n, batch;
+    long long ld, batch_pitch; // elements
+    int vec;                   // rows can be read eight elements at a time
+    float eps;
+    float2 *partial; // [batch][parts]
+    int parts;
+    float *f; // [batch]
+    __half *X; // planes of r x pitch, scaled by kScaleX
+    int planes, write_planes, pitch;
+};
+
+constexpr int kNormThreads = 256;
+
+// Eight consecutive elements j .. j+7 of a row of n, zero past its end.
+__device__ __forceinline__ void load8(const Input &p, long long row_at, int j, float (&v)[8])
+{
+    if (p.vec && j + 8 <= p.n) {
+        if (p.bf16) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.G) + row_at + j);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[2 * e] = __uint_as_float(w[e] << 16);
+                v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+            }
+        } else {
+            const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p.G) + row_at + j);
+            const float4 a = q[0], b = q[1];
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = j + e < p.n ? load_f32(p.G, p.bf16, row_at + j + e) : 0.0f;
+    }
+}
+
+// Sums of squares, and of the squares of 2^-96 times the elements for the
+// norm of a G whose squares overflow float32.
+__global__ void __launch_bounds__(kNormThreads) norm_kernel(const Input p)
+{
+    __shared__ float2 scratch[kNormThreads / 32];
+    const int b = blockIdx.y;
+    const unsigned units = static_cast<unsigned>((p.n + 7) / 8);
+    const unsigned total = units * static_cast<unsigned>(p.m);
+    constexpr float kDown = 1.26217744835361889e-29f; // 2^-96
+    float s = 0.0f, t = 0.0f;
+    for (unsigned u = blockIdx.x * kNormThreads + threadIdx.x; u < total; u += gridDim.x * kNormThreads) {
+        const unsigned row = u / units;
+        float v[8];
+        load8(p, b * p.batch_pitch + row * p.ld, static_cast<int>(u - row * units) * 8, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            s = fmaf(v[e], v[e], s);
+            const float d = v[e] * kDown;
+            t = fmaf(d, d, t);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        t += __shfl_xor_sync(0xffffffffu, t, o);
+    }
+    if (threadIdx.x % 32 == 0)
+        scratch[threadIdx.x / 32] = make_float2(s, t);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s = t = 0.0f;
+        for (int w = 0; w < kNormThreads / 32; ++w) {
+            s += scratch[w].x;
+            t += scratch[w].y;
+        }
+        p.partial[static_cast<long long>(b) * p.parts + blockIdx.x] = make_float2(s, t);
+    }
+}
+
+// X's planes from a 64 x 64 piece of G (transposed where G is tall), after
+// the norm from the partial sums: G times the power of two in
+// 1 / (|G|_F + eps), and f, the rest of it.
+template <bool Tall>
+__global__ void __launch_bounds__(kNormThreads) planes_kernel(const Input p)
+{
+    __shared__ float scale[2];
+    __shared__ float piece[Tall ? 64 : 1][65];
+    const int b = blockIdx.z;
+    grid_launch_next();
+    grid_wait();
+    if (threadIdx.x < 32) {
+        float s = 0.0f, t = 0.0f;
+        for (int k = threadIdx.x; k < p.parts; k += 32) {
+            const float2 v = p.partial[static_cast<long long>(b) * p.parts + k];
+            s += v.x;
+            t += v.y;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+            t += __shfl_xor_sync(0xffffffffu, t, o);
+        }
+        if (threadIdx.x == 0) {
+            // 1 / (|G|_F + eps) = inv 2^shift; an infinite or NaN norm makes
+            // every element NaN.
+            const bool big = !(s < __int_as_float(0x7f800000));
+            const float norm = big ? sqrtf(t) : sqrtf(s);
+            const float inv = big ? 1.0f / (norm + p.eps * 1.26217744835361889e-29f) : 1.0f / (norm + p.eps);
+            int e = 0;
+            float f = __int_as_float(0x7fc00000);
+            if (norm < __int_as_float(0x7f800000) && inv < __int_as_float(0x7f800000)) {
+                e = ilogbf(inv);
+                f = scalbnf(inv, -e);
+                e += (big ? -96 : 0) + 14; // kScaleX
+            }
+            scale[0] = scalbnf(1.0f, e / 2);
+            scale[1] = scalbnf(1.0f, e - e / 2);
+            if (blockIdx.x == 0 && blockIdx.y == 0)
+                p.f[b] = f;
+        }
+    }
+    __syncthreads();
+    const float s0 = scale[0], s1 = scale[1];
+    const int r = Tall ? p.n : p.m, c = Tall ? p.m : p.n;
+    const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
+    const int ty = threadIdx.x / 8, tx = threadIdx.x % 8 * 8;
+    const long long first = b * p.batch_pitch;
+    if constexpr (Tall) {
+#pragma unroll
+        for (int h = 0; h < 64; h += 32) {
+            float v[8];
+            if (j0 + ty + h < c) {
+                load8(p, first + (j0 + ty + h) * p.ld, i0 + tx, v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                piece[tx + e][ty + h] = v[e];
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int h = 0; h < 64; h += 32) {
+        const int i = i0 + ty + h;
+        if (i >= r)
+            break;
+        float v[8];
+        if constexpr (Tall) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = piece[ty + h][tx + e];
+        } else {
+            load8(p, first + i * p.ld, j0 + tx, v);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = v[e] * s0 * s1;
+        __half *x = p.X + (static_cast<long long>(b) * p.planes * r + i) * p.pitch + j0 + tx;
+        for (int q = 0; q < p.write_planes; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                w[e] = pack_f16(v[2 * e], v[2 * e + 1]);
+                const float2 kept = unpack_f16(w[e]);
+                v[2 * e] -= kept.x;
+                v[2 * e + 1] -= kept.y;
+            }
+            *reinterpret_cast<uint4 *>(x + static_cast<long long>(q) * r * p.pitch) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// ------------------------------------------------------------ host side
+struct Layout {
+    int r, c, rp, cp;   // sizes and 128-byte row pitches in elements
+    int xp, ap;         // planes of X; full planes of A and of Q
+    int parts;
+    size_t partial, f, x[2], a, a_diag, q, q_diag, total;
+};
+
+Layout make_layout(int batch, int m, int n, int out_dtype, int sms)
+{
+    Layout l;
+    l.r = std::min(m, n);
+    l.c = std::max(m, n);
+    l.rp = (l.r + 63) / 64 * 64;
+    l.cp = (l.c + 63) / 64 * 64;
+    l.xp = out_dtype == GEMM_DTYPE_F32 ? 3 : 2;
+    l.ap = out_dtype == GEMM_DTYPE_F32 ? 2 : 1;
+    // Enough CTAs for the norm to draw on the whole memory system, none with
+    // less than a few vectors per thread.
+    const long long units = (static_cast<long long>(m) * n + 8 * kNormThreads - 1) / (8 * kNormThreads);
+    l.parts = static_cast<int>(std::max(1ll, std::min<long long>(units, std::max(1, 4 * sms / batch))));
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    const size_t nb = static_cast<size_t>(batch);
+    l.partial = take(nb * l.parts * sizeof(float2));
+    l.f = take(nb * 4);
+    for (size_t &x : l.x)
+        x = take(nb * l.xp * l.r * l.cp * 2);
+    l.a = take(nb * l.ap * l.r * l.rp * 2);
+    l.a_diag = take(nb * l.r * kDiagBlock * 2);
+    l.q = take(nb * l.ap * l.r * l.rp * 2);
+    l.q_diag = take(nb * l.r * kDiagBlock * 2);
+    l.total = at;
+    return l;
+}
+
+// A matrix of planes in the workspace: r rows, `pitch` elements apart.
+struct Planes {
+    void *base;
+    int rows, cols, pitch, planes; // planes: over the whole batch
+};
+
+int encode(CUtensorMap *map, const Planes &m, int box_cols, int box_rows, bool swizzle)
+{
+    return encode_tensor_map_3d(map, kElement16, m.base, m.cols, m.rows, m.planes, static_cast<uint64_t>(m.pitch) * 2u,
+                                static_cast<uint64_t>(m.pitch) * 2u * m.rows, box_cols, box_rows, swizzle);
+}
+
+template <class Kernel, class... Args>
+int launch(Kernel kernel, dim3 grid, int threads, int smem, bool overlap, cudaStream_t s, const Args &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+struct Device {
+    int index, sms;
+    unsigned long long ctx;
+};
+
+template <int MH, int BN, int S, bool RightMN>
+int launch_product_t(const Maps &maps, const Product &p, const Device &d, cudaStream_t s)
+{
+    using T = Tile<MH, BN, S>;
+    static std::atomic<unsigned long long> limit_set[kMaxDevices];
+    if (ensure_smem_limit(product_kernel<MH, BN, S, RightMN>, T::kSmem, d.index, d.ctx, limit_set) != GEMM_OK)
+        return GEMM_ERR_CUDA;
+    const long long tiles = static_cast<long long>(tiles_of(p.symmetric != 0, (p.rows + T::BM - 1) / T::BM,
+                                                            (p.cols + BN - 1) / BN)) * p.batch;
+    const unsigned grid = static_cast<unsigned>(std::min<long long>(tiles, d.sms));
+    return launch(product_kernel<MH, BN, S, RightMN>, dim3(grid), T::kThreads, T::kSmem, true, s, maps, p);
+}
+
+// 256 x 256 tiles feed each right-hand slice to two MMAs, 128 x 128 ones
+// leave fewer SMs idle when there are few.
+bool use_large_tile(const Product &p, int sms)
+{
+    auto rounds = [&](int side) {
+        const long long tiles = static_cast<long long>(tiles_of(p.symmetric != 0, (p.rows + side - 1) / side,
+                                                                (p.cols + side - 1) / side)) * p.batch;
+        return (tiles + sms - 1) / sms;
+    };
+    return !p.fine && rounds(256) * 4 * 2 <= rounds(128) * 3;
+}
+
+template <bool RightMN>
+int launch_product(const Maps &maps, const Product &p, const Device &d, cudaStream_t s)
+{
+    return use_large_tile(p, d.sms) ? launch_product_t<2, 256, 3, RightMN>(maps, p, d, s)
+                                    : launch_product_t<1, 128, 4, RightMN>(maps, p, d, s);
+}
+
+struct Call {
+    int batch, m, n;
+    const void *G;
+    long long ldg, g_batch;
+    int dtype;
+    void *out;
+    long long ldo, o_batch;
+    int out_dtype;
+    int steps;
+    const float *coefficients;
+    float eps;
+};
+
+int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigned int *status, cudaStream_t s)
+{
+    const bool wide_result = call.out_dtype == GEMM_DTYPE_F32;
+    const bool tall = call.m > call.n;
+    const int nb = call.batch;
+    const Planes x[2] = {{ws + l.x[0], l.r, l.c, l.cp, nb * l.xp}, {ws + l.x[1], l.r, l.c, l.cp, nb * l.xp}};
+    const Planes a{ws + l.a, l.r, l.r, l.rp, nb * l.ap}, q{ws + l.q, l.r, l.r, l.rp, nb * l.ap};
+    const Planes a_diag{ws + l.a_diag, l.r, kDiagBlock, kDiagBlock, nb};
+    const Planes q_diag{ws + l.q_diag, l.r, kDiagBlock, kDiagBlock, nb};
+    float *f = reinterpret_cast<float *>(ws + l.f);
+
+    Maps from_x[2], from_a, from_qx[2]; // X X^T -> A (or Q); A A -> Q; Q X -> X
+    alignas(64) CUtensorMap to_out;
+    int st = GEMM_OK;
+    auto enc = [&](CUtensorMap *map, const Planes &m, int cols, int rows, bool swizzle) {
+        if (st == GEMM_OK)
+            st = encode(map, m, cols, rows, swizzle);
+    };
+    std::memset(&from_a, 0, sizeof from_a);
+    enc(&from_a.left, a, kBox, kBox, true);
+    enc(&from_a.left_diag, a_diag, kBox, kBox, true);
+    from_a.right = from_a.left;
+    from_a.right_diag = from_a.left_diag;
+    enc(&from_a.store, q, 64, 32, true);
+    enc(&from_a.mirror, q, 32, 64, false);
+    enc(&from_a.store_diag, q_diag, 64, 32, true);
+    enc(&from_a.mirror_diag, q_diag, 32, 64, false);
+    Maps to_a = from_a; // the stores into A
+    enc(&to_a.store, a, 64, 32, true);
+    enc(&to_a.mirror, a, 32, 64, false);
+    enc(&to_a.store_diag, a_diag, 64, 32, true);
+    enc(&to_a.mirror_diag, a_diag, 32, 64, false);
+    CUtensorMap q_load, q_diag_load;
+    enc(&q_load, q, kBox, kBox, true);
+    enc(&q_diag_load, q_diag, kBox, kBox, true);
+    for (int i = 0; i < 2; ++i) {
+        from_x[i] = to_a;
+        enc(&from_x[i].left, x[i], kBox, kBox, true);
+        from_x[i].right = from_x[i].left;
+        from_qx[i] = from_a;
+        from_qx[i].left = q_load;
+        from_qx[i].left_diag = q_diag_load;
+        from_qx[i].right = from_x[i].right;
+        enc(&from_qx[i].store, x[1 - i], 64, 32, true);
+    }
+    if (st != GEMM_OK)
+        return st;
+    const uint64_t es = wide_result ? 4 : 2;
+    const bool out_tma = (reinterpret_cast<uintptr_t>(call.out) & 15u) == 0 && (call.ldo * es) % 16 == 0 &&
+                         (nb == 1 || (call.o_batch * es) % 16 == 0);
+    std::memset(&to_out, 0, sizeof to_out);
+    if (out_tma) {
+        const uint64_t plane_pitch = nb == 1 ? call.ldo * es * static_cast<uint64_t>(call.m) : call.o_batch * es;
+        const uint32_t box_cols = wide_result || tall ? 32 : 64, box_rows = tall && !wide_result ? 64 : 32;
+        st = encode_tensor_map_3d(&to_out, wide_result ? kElement32 : kElement16, call.out, call.n, call.m, nb,
+                                  call.ldo * es, plane_pitch, box_cols, box_rows, !tall);
+        if (st != GEMM_OK)
+            return st;
+    }
+
+    // Norm and the first iterate.  A bfloat16 G is exact in one plane.
+    const bool exact_input = call.dtype == GEMM_DTYPE_BF16;
+    Input in{call.G, call.dtype == GEMM_DTYPE_BF16, call.m, call.n, nb, call.ldg, call.g_batch, 0, call.eps,
+             reinterpret_cast<float2 *>(ws + l.partial), l.parts, f, static_cast<__half *>(x[0].base), l.xp,
+             exact_input ? 1 : l.xp, l.cp};
+    const uint64_t gs = call.dtype == GEMM_DTYPE_F32 ? 4 : 2;
+    in.vec = (reinterpret_cast<uintptr_t>(call.G) & 15u) == 0 && (call.ldg * gs) % 16 == 0 &&
+             (nb == 1 || (call.g_batch * gs) % 16 == 0);
+    st = launch(norm_kernel, dim3(l.parts, nb), kNormThreads, 0, false, s, in);
+    if (st != GEMM_OK)
+        return st;
+    const dim3 pieces((l.c + 63) / 64, (l.r + 63) / 64, nb);
+    st = tall ? launch(planes_kernel<true>, pieces, kNormThreads, 0, true, s, in)
+              : launch(planes_kernel<false>, pieces, kNormThreads, 0, true, s, in);
+    if (st != GEMM_OK)
+        return st;
+
+    Product base = {};
+    base.batch = nb;
+    base.f = f;
+    base.status = status;
+    base.wait_limit_ns = call_wait_limit_ns();
+    base.withhold = call_withhold();
+    base.fine = wide_result;
+    for (int step = 0; step < call.steps; ++step) {
+        const float ca = call.coefficients[3 * step], cb = call.coefficients[3 * step + 1],
+                    cc = call.coefficients[3 * step + 2];
+        const bool first = step == 0, last = step == call.steps - 1;
+        const bool one_plane = first && exact_input; // X has no more than that
+        const int cur = step & 1;
+        auto add = [](Product &p, int left, int right, Range range) {
+            p.pass[p.passes++] = Pass{static_cast<signed char>(left), static_cast<signed char>(right),
+                                      static_cast<signed char>(range)};
+        };
+
+        // X X^T: to A + (b / 2c) I, or with c = 0 to Q itself.
+        Product p = base;
+        p.rows = p.cols = l.r;
+        p.k = l.c;
+        p.symmetric = 1;
+        p.left_planes = p.right_planes = l.xp;
+        if (wide_result && !one_plane) {
+            add(p, 0, 1, kAll);
+            add(p, 1, 0, kAll);
+        }
+        add(p, 0, 0, kAll);
+        p.output = kPlanes;
+        p.planes = p.planes_pitch = l.ap;
+        p.diag_plane = 1;
+        if (cc != 0.0f) {
+            p.alpha = kScaleA / (kScaleX * kScaleX);
+            p.diag = kScaleA * (cb / (2.0f * cc));
+            p.alpha_power = first ? 2 : 0;
+        } else {
+            p.alpha = kScaleQ * cb / (kScaleX * kScaleX);
+            p.diag = kScaleQ * ca;
+            p.alpha_power = first ? 3 : 0;
+            p.diag_power = first ? 1 : 0;
+        }
+        Maps maps = from_x[cur];
+        if (cc == 0.0f) {
+            maps.store = from_a.store;
+            maps.mirror = from_a.mirror;
+            maps.store_diag = from_a.store_diag;
+            maps.mirror_diag = from_a.mirror_diag;
+        }
+        st = launch_product<false>(maps, p, d, s);
+        if (st != GEMM_OK)
+            return st;
+
+        if (cc != 0.0f) {
+            // The square, to Q.
+            p = base;
+            p.rows = p.cols = p.k = l.r;
+            p.symmetric = 1;
+            p.left_planes = p.right_planes = l.ap;
+            add(p, 0, -1, kCols);
+            add(p, -1, 0, kRows);
+            if (wide_result) {
+                add(p, 0, 1, kAll);
+                add(p, 1, 0, kAll);
+            }
+            add(p, 0, 0, kAll);
+            p.output = kPlanes;
+            p.planes = p.planes_pitch = l.ap;
+            p.diag_plane = 1;
+            p.alpha = kScaleQ * cc / (kScaleA * kScaleA);
+            p.diag = kScaleQ * static_cast<float>(ca - static_cast<double>(cb) * cb / (4.0 * cc));
+            p.alpha_power = p.diag_power = first ? 1 : 0;
+            st = launch_product<false>(from_a, p, d, s);
+            if (st != GEMM_OK)
+                return st;
+        }
+
+        // Q X: to the next X, or to the result.
+        p = base;
+        p.rows = p.k = l.r;
+        p.cols = l.c;
+        p.left_planes = l.ap;
+        p.right_planes = l.xp;
+        add(p, -1, 0, kRows);
+        if (wide_result) {
+            if (!one_plane) {
+                if (!last) {
+                    add(p, 0, 2, kAll);
+                    add(p, 1, 1, kAll);
+                }
+                add(p, 0, 1, kAll);
+            }
+            add(p, 1, 0, kAll);
+        } else if (!one_plane && !last) {
+            add(p, 0, 1, kAll);
+        }
+        add(p, 0, 0, kAll);
+        maps = from_qx[cur];
+        if (last) {
+            p.output = wide_result ? kF32 : kBf16;
+            p.alpha = 1.0f / (kScaleQ * kScaleX);
+            p.transposed = tall;
+            p.out_tma = out_tma;
+            p.out = call.out;
+            p.ldo = call.ldo;
+            p.out_batch = call.o_batch;
+            maps.store = to_out;
+        } else {
+            p.output = kPlanes;
+            // The last step reads one plane less.
+            p.planes = step == call.steps - 2 ? l.xp - 1 : l.xp;
+            p.planes_pitch = l.xp;
+            p.alpha = 1.0f / kScaleQ;
+        }
+        st = launch_product<true>(maps, p, d, s);
+        if (st != GEMM_OK)
+            return st;
+    }
+    return GEMM_OK;
+}
+
+// Whether the iteration stays where the planes can hold it: from singular
+// values in [0, 1], every step's values within [0, 2] and Q within 15
+// (30 with the first step's f below 2).
+int check_coefficients(const float *coefficients, int steps)
+{
+    double top = 1.0;
+    for (int k = 0; k < steps; ++k) {
+        const double a = coefficients[3 * k], b = coefficients[3 * k + 1], c = coefficients[3 * k + 2];
+        if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
+            return GEMM_ERR_INVALID_ARG;
+        if (c != 0.0 && std::fabs(b) > 8.0 * std::fabs(c))
+            return GEMM_ERR_UNSUPPORTED; // completing the square would cancel
+        double next = 0.0;
+        constexpr int kSamples = 256;
+        for (int i = 0; i <= kSamples; ++i) {
+            const double x = top * i / kSamples, y = x * x;
+            const double q = a + b * y + c * y * y;
+            if (std::fabs(q) > 15.0)
+                return GEMM_ERR_UNSUPPORTED;
+            next = std::max(next, std::fabs(x * q));
+        }
+        if (next > 1.99)
+            return GEMM_ERR_UNSUPPORTED;
+        top = next;
+    }
+    return GEMM_OK;
+}
+
+bool valid_dtype(int d) { return d == GEMM_DTYPE_F32 || d == GEMM_DTYPE_BF16; }
+
+constexpr int kMaxSteps = 32;
+constexpr int kMaxSide = 1 << 20;
+constexpr long long kMaxElements = 0x7fffffffll;
+constexpr int kMaxBatch = 65535;
+
+int check_sizes(int batch, int m, int n)
+{
+    if (batch < 0 || m < 0 || n < 0)
+        return GEMM_ERR_INVALID_ARG;
+    if (batch > kMaxBatch || m > kMaxSide || n > kMaxSide || static_cast<long long>(m) * n > kMaxElements)
+        return GEMM_ERR_UNSUPPORTED;
+    // Tiles of the whole batch are counted in an int.
+    const long long tiles = (static_cast<long long>(m) + 127) / 128 * ((n + 127) / 128) * batch;
+    return tiles > 0x3fffffffll ? GEMM_ERR_UNSUPPORTED : GEMM_OK;
+}
+
+} // namespace orth
+
+} // namespace pg
+
+using namespace pg;
+
+extern "C" {
+
+int orthogonalize_workspace(int batch, int m, int n, int out_dtype, size_t *bytes)
+{
+    if (!bytes || !orth::valid_dtype(out_dtype))
+        return GEMM_ERR_INVALID_ARG;
+    const int st = orth::check_sizes(batch, m, n);
+    if (st != GEMM_OK)
+        return st;
+    *bytes = batch == 0 || m == 0 || n == 0 ? 0 : orth::make_layout(batch, m, n, out_dtype, device_sms()).total;
+    return GEMM_OK;
+}
+
+int orthogonalize(int batch, int m, int n, const void *G, long long ldg, long long g_batch, int dtype, void *out,
+                  long long ldo, long long o_batch, int out_dtype, int steps, const float *coefficients, float eps,
+                  void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!orth::valid_dtype(dtype) || !orth::valid_dtype(out_dtype) || steps < 1 || steps > orth::kMaxSteps ||
+        !coefficients || !(eps >= 0.0f) || !std::isfinite(eps))
+        return GEMM_ERR_INVALID_ARG;
+    int st = orth::check_sizes(batch, m, n);
+    if (st != GEMM_OK)
+        return st;
+    st = orth::check_coefficients(coefficients, steps);
+    if (st != GEMM_OK)
+        return st;
+    const bool empty = batch == 0 || m == 0 || n == 0;
+    if (!empty) {
+        if (ldg < n || ldo < n || !G || !out)
+            return GEMM_ERR_INVALID_ARG;
+        if (batch > 1 && (g_batch < 0 || o_batch < ldo * (m - 1) + n))
+            return GEMM_ERR_INVALID_ARG;
+        const uintptr_t ga = dtype == GEMM_DTYPE_F32 ? 3u : 1u, oa = out_dtype == GEMM_DTYPE_F32 ? 3u : 1u;
+        if ((reinterpret_cast<uintptr_t>(G) & ga) != 0 || (reinterpret_cast<uintptr_t>(out) & oa) != 0 ||
+            (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+            return GEMM_ERR_MISALIGNED;
+    }
+    int dev;
+    st = device_checked(&dev);
+    if (st != GEMM_OK)
+        return st;
+    if (empty)
+        return GEMM_OK;
+    const orth::Device d{dev, device_sms(), current_context_id()};
+    const orth::Layout l = orth::make_layout(batch, m, n, out_dtype, d.sms);
+    if (!workspace || workspace_bytes < l.total)
+        return GEMM_ERR_INVALID_ARG;
+    unsigned int *status = device_status_word(dev, d.ctx);
+    if (!status)
+        return GEMM_ERR_CUDA;
+    const orth::Call call{batch, m, n, G, ldg, g_batch, dtype, out, ldo, o_batch, out_dtype, steps, coefficients, eps};
+    return orth::run(call, l, static_cast<uint8_t *>(workspace), d, status, static_cast<cudaStream_t>(stream));
+}
+
+} // extern "C"

@@ -3,6 +3,7 @@
     y, mean, rstd = pg.layer_norm(x, weight, bias, stats=True)
     C = pg.gemm_bf16(y, W)                                       # the projection itself
     dx, dweight, dbias = pg.layer_norm_backward(dy, x, mean, rstd, weight)
+    update = pg.orthogonalize(momentum, dtype=torch.bfloat16)    # the orthogonalised step for W
 
 Argument checks and marshalling only; the kernels are in the CUDA library.
 CUDA tensors in, CUDA tensors out, enqueued on `stream` (default: torch's
@@ -14,7 +15,7 @@ import ctypes
 
 import async_copy_pipelined_gb300 as _pg
 
-__all__ = ["layer_norm", "layer_norm_backward"]
+__all__ = ["layer_norm", "layer_norm_backward", "orthogonalize"]
 
 F32, BF16 = 0, 1  # enum gemm_dtype
 
@@ -29,6 +30,10 @@ def bind(l):
     l.layer_norm_backward_workspace.restype = I
     l.layer_norm_backward.argtypes = [I, I, P, L, P, L, I, P, P, P, I, P, L, P, P, P, S, P]
     l.layer_norm_backward.restype = I
+    l.orthogonalize_workspace.argtypes = [I, I, I, I, ctypes.POINTER(S)]
+    l.orthogonalize_workspace.restype = I
+    l.orthogonalize.argtypes = [I, I, I, P, L, L, I, P, L, L, I, I, ctypes.POINTER(F), F, P, S, P]
+    l.orthogonalize.restype = I
     return l
 
 
@@ -254,3 +259,82 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, *, stream=None
     _pg._check(st, "layer_norm_backward")
     _record(other, dy, x, mean, rstd, weight, out, dweight)
     return out, dweight, dbias
+
+
+# Singular values from (0, 1] to around 1 in five steps: the quintic of the
+# widest use, steep at zero (a = 3.44) at the price of ending within 0.68 .. 1.2.
+COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def _matrices(t, name):
+    """(batch, m, n, row pitch, matrix pitch) of one matrix or a stack."""
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be a matrix or a stack of matrices")
+    m, n = t.shape[-2:]
+    batch = t.shape[0] if t.dim() == 3 else 1
+    if t.numel() == 0:
+        return batch, m, n, max(n, 1), max(m * n, 1)
+    if n > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit column stride (row-major rows)")
+    pitch = t.stride(-2) if m > 1 else n
+    if pitch < n:
+        raise ValueError(f"the rows of {name} overlap in memory")
+    return batch, m, n, pitch, t.stride(0) if batch > 1 else pitch * (m - 1) + n
+
+
+def orthogonalize(G, out=None, *, steps=5, coefficients=COEFFICIENTS, eps=1e-7, dtype=None, workspace="auto",
+                  stream=None):
+    """The orthogonalised form of a weight's update G, by Newton-Schulz products.
+
+    X <- G / (|G|_F + eps), then `steps` times X <- a X + (b A + c A A) X with
+    A = X X^T (on the shorter side of G).  G: one matrix or a stack of them,
+    float32 or bfloat16, rows at any pitch.  The result has G's shape and
+    `dtype` (default: G's), which also sets the precision of the products: a
+    bfloat16 result is within a small part of bfloat16's rounding of the
+    exact one, a float32 result near what float32 arithmetic gives, at about
+    three times the cost.
+
+    coefficients: one (a, b, c) for every step, or `steps` of them.  out:
+    where the result goes (G itself for an in-place call).  workspace: "auto"
+    keeps one buffer per device and stream, grown as needed; or a uint8 CUDA
+    tensor of at least orthogonalize_workspace() bytes (the C header)."""
+    import torch
+    dt = _dtype(G, "G")
+    batch, m, n, ldg, g_batch = _matrices(G, "G")
+    device = G.device
+    handle, other = _enter(device, stream)
+    if out is None:
+        dtype = G.dtype if dtype is None else dtype
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"dtype must be float32 or bfloat16, not {dtype}")
+        out = torch.empty(G.shape, dtype=dtype, device=device)
+    elif out.device != device:
+        raise ValueError(f"out is on {out.device}, G on {device}: all operands must be on one device")
+    elif out.shape != G.shape or (dtype is not None and out.dtype != dtype):
+        raise ValueError("out must have G's shape and the type asked for")
+    odt = _dtype(out, "out")
+    _, _, _, ldo, o_batch = _matrices(out, "out")
+    if batch > 1 and out.numel() and o_batch < ldo * (m - 1) + n:
+        raise ValueError("the matrices of out overlap in memory")
+    triples = [float(v) for c in (coefficients if hasattr(coefficients[0], "__len__") else [coefficients] * steps)
+               for v in c]
+    if len(triples) != 3 * steps or steps < 1:
+        raise ValueError("coefficients must be one (a, b, c), or one for each of one or more steps")
+    l = _pg.lib()
+    with _on(device):
+        need = ctypes.c_size_t()
+        _pg._check(l.orthogonalize_workspace(batch, m, n, odt, ctypes.byref(need)), "orthogonalize_workspace")
+        if isinstance(workspace, str):
+            if workspace != "auto":
+                raise ValueError('workspace must be "auto" or a uint8 CUDA tensor')
+            ws = _workspace("orthogonalize", device, handle, need.value, other)
+        else:
+            ws = workspace
+            if ws.device != device:
+                raise ValueError(f"workspace is on {ws.device}, G on {device}")
+        st = l.orthogonalize(batch, m, n, G.data_ptr(), ldg, g_batch, dt, out.data_ptr(), ldo, o_batch, odt, steps,
+                             (ctypes.c_float * len(triples))(*triples), eps, ws.data_ptr(),
+                             ws.numel() * ws.element_size(), handle)
+    _pg._check(st, "orthogonalize")
+    _record(other, G, out, ws)
+    return out

@@ -97,6 +97,54 @@ int layer_norm_backward(int rows, int cols,
  * (a 152-SM part where no device can be asked). */
 int layer_norm_backward_workspace(int rows, int cols, size_t *bytes);
 
+/*
+ * orthogonalize: the orthogonalised form of a weight's update, by
+ * Newton-Schulz products.  For each m x n matrix G of a batch, with X seen
+ * on its shorter side (X^T is iterated where m > n, which gives the same):
+ *
+ *   X <- G / (|G|_F + eps)
+ *   steps times:  A = X X^T;   X <- a X + (b A + c A A) X
+ *   out = X
+ *
+ * With (a, b, c) = (3.4445, -4.7750, 2.0315) five steps take every singular
+ * value that is not tiny beside |G|_F to somewhere in 0.68 .. 1.2 and keep the
+ * singular vectors.
+ *
+ *   batch, m, n   matrices and their sizes, each >= 0 (any of them 0: nothing
+ *                 is done); sides to 2^20, m n below 2^31, batch to 65535.
+ *   G             matrix b, element (i, j) at G[b*g_batch + i*ldg + j], of
+ *                 `dtype`; ldg >= n, any alignment.  It is read whole before
+ *                 anything is written to out.
+ *   out           likewise with ldo, o_batch, of `out_dtype`; may be G
+ *                 itself.  The products run in the precision this type asks
+ *                 for: on GB300 the tensor cores' float16 pairs, with
+ *                 float32 sums, whose error stays below bfloat16's rounding
+ *                 for GEMM_DTYPE_BF16 and near float32 arithmetic's for
+ *                 GEMM_DTYPE_F32 (at about three times the time).
+ *   steps         1 .. 32.
+ *   coefficients  3 * steps floats in host memory: a, b, c of each step.
+ *                 c = 0 or |b| <= 8 |c|, and from singular values in [0, 1]
+ *                 no step may leave [-1.99, 1.99], or reach 15 in
+ *                 a + b s + c s s; else GEMM_ERR_UNSUPPORTED.
+ *   eps           >= 0, finite.  A zero G gives zeros (NaN with eps 0).
+ *   workspace     device memory of at least orthogonalize_workspace() bytes,
+ *                 256-byte aligned; needs no initialisation, holds nothing
+ *                 between calls, serves one call at a time.
+ *
+ * A matrix that holds a NaN or an infinity comes out as NaN throughout; the
+ * others of the batch are not touched by it.
+ */
+int orthogonalize(int batch, int m, int n,
+                  const void *G, long long ldg, long long g_batch, int dtype,
+                  void *out, long long ldo, long long o_batch, int out_dtype,
+                  int steps, const float *coefficients, float eps,
+                  void *workspace, size_t workspace_bytes,
+                  void *stream);
+
+/* Bytes orthogonalize needs for these sizes on the current device (a 152-SM
+ * part where no device can be asked). */
+int orthogonalize_workspace(int batch, int m, int n, int out_dtype, size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

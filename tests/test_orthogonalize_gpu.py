@@ -1,0 +1,287 @@
+"""Newton-Schulz orthogonalisation against float64.
+
+Tolerances, as |got - exact|_F / |exact|_F.  The exact iteration in float64
+multiplies a perturbation of the iterate by at most the polynomial's slope in
+each direction, so the floor of any arithmetic with unit roundoff u is a small
+multiple of u and depends on the spectrum; what the planes keep is u = 2^-11
+(one float16 plane) beyond which X's extra plane and the diagonal's carry
+eleven bits more.
+
+  bfloat16 result: rounding the exact result alone errs by at most 2^-8 per
+  element, in the mean by 2^-8 / sqrt(12) * 1.44 = 0.0017 (uniform mantissas).
+  The result must be within 1.3 times that: 0.0022; of fewer than 1024
+  elements, whose mean says little, 1.3 times 2^-8.
+  float32 result: 2^-22 per product (two planes hold 22 bits), five steps of
+  three products and a gain of up to 3.4445 a step on what is lost early: at
+  most 5 * 3 * 2^-22 * 3.4445^2 = 4.2e-5 where small singular values are
+  present, and 2e-5 for the well-conditioned matrices below."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+TRIPLE = (3.4445, -4.7750, 2.0315)
+
+
+def _tol(out, x):
+    return 4.2e-5 if out == "f32" else 0.0022 if x.numel() >= 1024 else 1.3 * 2.0 ** -8
+
+
+def _torch_dtype(dtype):
+    import torch
+    return {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+
+
+def _exact(g, steps=5, coefficients=TRIPLE, eps=1e-7):
+    """float64, on the device for speed: g (m x n) as given."""
+    x = g.double()
+    tall = x.shape[0] > x.shape[1]
+    x = x.T if tall else x
+    x = x / (x.square().sum().sqrt() + eps)
+    for k in range(steps):
+        a, b, c = coefficients if not hasattr(coefficients[0], "__len__") else coefficients[k]
+        s = x @ x.T
+        x = a * x + (b * s + c * (s @ s)) @ x
+    return x.T if tall else x
+
+
+def _rel(got, want):
+    d = got.double() - want
+    return (d.square().sum().sqrt() / want.square().sum().sqrt()).item()
+
+
+def _gradient(m, n, kind, seed, scale=1e-3):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((m, n), generator=g, device="cuda")
+    if kind == "decay":  # strong directions over a weak floor
+        k = max(1, min(m, n) // 8)
+        left = torch.randn((m, k), generator=g, device="cuda") * torch.arange(1, k + 1, device="cuda") ** -1.0
+        x = 0.05 * x + left @ torch.randn((k, n), generator=g, device="cuda")
+    return x * scale
+
+
+def _check_status():
+    import async_copy_pipelined_gb300 as pg
+    assert pg.device_status() == (0, 0)
+
+
+SHAPES = [(1, 1), (1, 7), (9, 1), (2, 3), (8, 8), (17, 33), (64, 64), (65, 63), (128, 128), (129, 127), (100, 300),
+          (300, 100), (256, 256), (255, 257), (257, 513), (640, 384), (1000, 1000), (1024, 768), (333, 2100),
+          (2100, 333), (1536, 1536), (2056, 3080)]
+
+
+@pytest.mark.parametrize("m,n", SHAPES)
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16"), ("bf16", "f32")])
+def test_against_float64(m, n, dtype, out):
+    import async_copy_pipelined_gb300 as pg
+    for kind in ("flat", "decay"):
+        g = _gradient(m, n, kind, m * 7 + n).to(_torch_dtype(dtype))
+        before = g.clone()
+        o = pg.orthogonalize(g, dtype=_torch_dtype(out))
+        assert o.shape == g.shape and o.dtype == _torch_dtype(out)
+        assert (g == before).all()
+        assert _rel(o, _exact(g)) <= _tol(out, g), kind
+        again = pg.orthogonalize(g, dtype=_torch_dtype(out))
+        assert (again == o).all()
+    _check_status()
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_is_orthogonal(out):
+    """Singular values of the result lie in 0.68 .. 1.2 and its singular
+    vectors are G's: O G^T is symmetric positive."""
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    g = _gradient(200, 500, "flat", 3)
+    o = pg.orthogonalize(g, dtype=_torch_dtype(out)).double()
+    s = torch.linalg.svdvals(o)
+    assert 0.66 < s.min() and s.max() < 1.22
+    p = o @ g.double().T
+    assert (p - p.T).norm() < 0.01 * p.norm() and torch.linalg.eigvalsh((p + p.T) / 2).min() > 0
+
+
+@pytest.mark.parametrize("batch,m,n", [(1, 40, 60), (3, 100, 260), (5, 260, 100), (12, 128, 128), (2, 700, 700),
+                                       (40, 33, 65)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f32", "f32")])
+def test_batch_equals_single_matrices(batch, m, n, dtype, out):
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    g = torch.stack([_gradient(m, n, "decay", 50 + b, scale=10.0 ** (b - 2)) for b in range(batch)])
+    g = g.to(_torch_dtype(dtype))
+    o = pg.orthogonalize(g, dtype=_torch_dtype(out))
+    for b in range(batch):
+        assert _rel(o[b], _exact(g[b])) <= _tol(out, g[b])
+    _check_status()
+
+
+@pytest.mark.parametrize("m,n", [(100, 300), (300, 100), (130, 130)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("pad,offset", [(0, 1), (3, 0), (8, 8), (5, 3)])
+def test_pitches_alignment_and_bounds(m, n, dtype, out, pad, offset):
+    """Column slices at any offset, for G and for out; nothing outside out's
+    elements is written."""
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    batch = 2
+
+    def slices(values, dt):
+        buf = torch.full((offset + batch * m * (n + pad),), 77.0, dtype=dt, device="cuda")
+        view = buf[offset:].view(batch, m, n + pad)[:, :, :n]
+        if values is not None:
+            view.copy_(values)
+        return buf, view
+
+    plain = torch.stack([_gradient(m, n, "decay", b) for b in range(batch)]).to(_torch_dtype(dtype))
+    want = pg.orthogonalize(plain, dtype=_torch_dtype(out))
+    _, g = slices(plain, plain.dtype)
+    buf, o = slices(None, _torch_dtype(out))
+    assert pg.orthogonalize(g, o) is o
+    assert torch.equal(o, want)
+    o.fill_(77.0)
+    assert (buf == 77.0).all()
+    if dtype == out:
+        pg.orthogonalize(g, g)  # in place
+        assert torch.equal(g, want)
+    _check_status()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1e-30, 1e-12, 1.0, 1e15, 1e25, 1e37])
+def test_scale_of_G(dtype, scale):
+    """From gradients whose squares vanish in float32 to ones whose squares
+    overflow it (eps 0 so that the smallest still count)."""
+    import async_copy_pipelined_gb300 as pg
+    g = _gradient(96, 160, "flat", 11, scale=1.0).clamp(-3, 3)
+    g = (g * scale).to(_torch_dtype(dtype))
+    if scale == 1e-30:
+        eps = 1e-28  # squares are zero in float32: the norm reads 0, X = G / eps
+        want = _exact(g * 0 + g, eps=1e-28)
+        got = pg.orthogonalize(g, eps=eps)
+        assert got.isfinite().all() and want.isfinite().all()
+        return
+    got = pg.orthogonalize(g, eps=0.0)
+    assert _rel(got, _exact(g, eps=0.0)) <= _tol(dtype, g)
+
+
+def test_zero_and_non_finite_matrices():
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    g = torch.stack([_gradient(130, 200, "flat", b) for b in range(5)])
+    clean = pg.orthogonalize(g)
+    g[1] = 0.0
+    g[2, 129, 199] = float("nan")
+    g[3, 0, 0] = float("inf")
+    o = pg.orthogonalize(g)
+    assert (o[1] == 0).all() and o[2].isnan().all() and o[3].isnan().all()
+    assert torch.equal(o[0], clean[0]) and torch.equal(o[4], clean[4])
+    b = pg.orthogonalize(g.bfloat16())
+    assert (b[1] == 0).all() and b[2].isnan().all() and b[3].isnan().all() and b[0].isfinite().all()
+    zeroed = _gradient(130, 200, "flat", 9)
+    zeroed[10:20] = 0.0
+    zeroed[:, 50] = 0.0
+    z = pg.orthogonalize(zeroed)
+    assert (z[10:20] == 0).all() and (z[:, 50] == 0).all() and _rel(z, _exact(zeroed)) <= _tol("f32", zeroed)
+    _check_status()
+
+
+def test_small_singular_values():
+    """16 directions at 1 over a floor at 1e-3: what one rounding to eleven
+    bits loses would come out hundreds of times larger."""
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    g = torch.Generator(device="cuda").manual_seed(2)
+    u = torch.linalg.qr(torch.randn((384, 384), generator=g, device="cuda").double())[0]
+    v = torch.linalg.qr(torch.randn((640, 384), generator=g, device="cuda").double())[0]
+    s = torch.full((384,), 1e-3, device="cuda", dtype=torch.float64)
+    s[:16] = 1.0
+    x = ((u * s) @ v.T).float()
+    for dt, out in (("bf16", "bf16"), ("f32", "bf16"), ("f32", "f32")):
+        gx = x.to(_torch_dtype(dt))
+        assert _rel(pg.orthogonalize(gx, dtype=_torch_dtype(out)), _exact(gx)) <= _tol(out, gx), (dt, out)
+
+
+@pytest.mark.parametrize("steps,coefficients", [
+    (1, TRIPLE), (2, TRIPLE), (3, TRIPLE), (9, (1.5, -0.5, 0.0)), (6, (1.875, -1.25, 0.375)), (1, (1.5, -0.5, 0.0)),
+    (3, [(3.4445, -4.7750, 2.0315), (1.5, -0.5, 0.0), (1.875, -1.25, 0.375)]), (2, (1.0, 0.0, 0.0)),
+])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_steps_and_coefficients(steps, coefficients, out):
+    import async_copy_pipelined_gb300 as pg
+    for m, n in ((150, 270), (270, 150)):
+        g = _gradient(m, n, "decay", steps).to(_torch_dtype(out))
+        o = pg.orthogonalize(g, steps=steps, coefficients=coefficients)
+        assert _rel(o, _exact(g, steps, coefficients)) <= _tol(out, g)
+
+
+def test_streams_graphs_and_workspace():
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    g = _gradient(300, 500, "decay", 1).bfloat16()
+    want = pg.orthogonalize(g)
+    s = torch.cuda.Stream()
+    o = pg.orthogonalize(g, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(o, want)
+    ws = torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")  # float16 NaN everywhere
+    assert torch.equal(pg.orthogonalize(g, workspace=ws), want)
+    graph = torch.cuda.CUDAGraph()
+    static = g.clone()
+    with torch.cuda.graph(graph):
+        captured = pg.orthogonalize(static, workspace=ws)
+    for k in range(3):
+        static.copy_(g if k != 1 else g.flip(0))
+        graph.replay()
+        assert torch.equal(captured, want if k != 1 else pg.orthogonalize(g.flip(0)))
+    _check_status()
+
+
+def test_refusals_on_device():
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    g = _gradient(64, 96, "flat", 1)
+    with pytest.raises(TypeError):
+        pg.orthogonalize(g.half())
+    with pytest.raises(TypeError):
+        pg.orthogonalize(g, dtype=torch.float16)
+    with pytest.raises(ValueError, match="stack of matrices"):
+        pg.orthogonalize(g[0])
+    with pytest.raises(ValueError, match="unit column stride"):
+        pg.orthogonalize(g.t())
+    with pytest.raises(ValueError, match="shape"):
+        pg.orthogonalize(g, g[:32])
+    with pytest.raises(ValueError, match="one device"):
+        pg.orthogonalize(g, torch.empty((64, 96)))
+    with pytest.raises(ValueError, match="coefficients"):
+        pg.orthogonalize(g, coefficients=[TRIPLE] * 4)
+    with pytest.raises(ValueError, match="overlap"):
+        pg.orthogonalize(torch.stack([g, g]), torch.empty_like(g).expand(2, 64, 96))
+    for kw, status in ((dict(steps=40), 1), (dict(eps=-1.0), 1), (dict(coefficients=(9.0, -8.0, 2.0)), 3),
+                       (dict(coefficients=(2.0, -1.0, 0.01)), 3), (dict(coefficients=(float("nan"), 0.0, 0.0)), 1),
+                       (dict(workspace=torch.empty(1024, dtype=torch.uint8, device="cuda")), 1)):
+        with pytest.raises(pg.GemmError) as e:
+            pg.orthogonalize(g, **kw)
+        assert e.value.status == status, kw
+    empty = pg.orthogonalize(torch.empty((0, 5), device="cuda"))
+    assert empty.shape == (0, 5)
+    assert pg.orthogonalize(torch.empty((0, 5, 6), device="cuda")).shape == (0, 5, 6)
+    torch.cuda.synchronize()
+    _check_status()
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """A ring position nothing fills: the kernels give up, say so, and the
+    next call is right."""
+    import async_copy_pipelined_gb300 as pg
+    g = _gradient(200, 300, "flat", 1)
+    want = pg.orthogonalize(g)
+    _check_status()
+    try:
+        pg.testing_set_hooks(20_000_000, 1)  # 20 ms
+        pg.orthogonalize(g)
+    finally:
+        pg.testing_set_hooks()
+    status, detail = pg.device_status()
+    assert status == 6 and detail & 0xFF == 7
+    assert (pg.orthogonalize(g) == want).all()
+    _check_status()

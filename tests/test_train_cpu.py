@@ -65,3 +65,44 @@ def test_host_tensors_are_refused(lib):
         pg.layer_norm_backward(x, x, torch.ones(4), torch.ones(4))
     with pytest.raises(TypeError):
         pg.layer_norm(x.double())
+
+
+def _orthogonalize(lib, batch=2, m=8, n=16, G=256, ldg=16, gb=128, dtype=0, out=512, ldo=16, ob=128, odt=0, steps=1,
+                   co=(1.5, -0.5, 0.0), eps=1e-7, ws=1024, ws_bytes=1 << 30):
+    arr = None if co is None else (ctypes.c_float * len(co))(*co)
+    return lib.orthogonalize(batch, m, n, G, ldg, gb, dtype, out, ldo, ob, odt, steps, arr, eps, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(batch=-1), INVALID), (dict(m=-1), INVALID), (dict(n=-5), INVALID), (dict(ldg=15), INVALID),
+    (dict(ldo=15), INVALID), (dict(ob=127), INVALID), (dict(gb=-1), INVALID), (dict(G=None), INVALID),
+    (dict(out=None), INVALID), (dict(dtype=2), INVALID), (dict(odt=-1), INVALID), (dict(steps=0), INVALID),
+    (dict(steps=33), INVALID), (dict(co=None), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID),
+    (dict(co=(float("inf"), 0.0, 0.0)), INVALID), (dict(co=(3.0, 0.0, 0.0)), 3), (dict(co=(2.0, -1.0, 0.1)), 3),
+    (dict(G=257), MISALIGNED), (dict(out=513, odt=1), MISALIGNED), (dict(ws=1040), MISALIGNED),
+    (dict(m=1 << 21, n=1), 3), (dict(m=1 << 16, n=1 << 16), 3),
+])
+def test_orthogonalize_validation(lib, kw, status):
+    assert _orthogonalize(lib, **kw) == status
+
+
+def test_orthogonalize_workspace(lib):
+    n = ctypes.c_size_t()
+    sizes = []
+    for dt in (1, 0):
+        assert lib.orthogonalize_workspace(1, 1000, 3000, dt, ctypes.byref(n)) == 0
+        sizes.append(n.value)
+    # two iterates of two planes, A and Q of one; three and two for float32
+    assert sizes[0] > 2 * 2 * 1000 * 3000 * 2 + 2 * 1000 * 1000 * 2
+    assert sizes[1] > 2 * 3 * 1000 * 3000 * 2 + 2 * 2 * 1000 * 1000 * 2
+    assert lib.orthogonalize_workspace(1, 3000, 1000, 0, ctypes.byref(n)) == 0 and n.value == sizes[1]
+    assert lib.orthogonalize_workspace(3, 0, 10, 0, ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.orthogonalize_workspace(1, -1, 10, 0, ctypes.byref(n)) == INVALID
+    assert lib.orthogonalize_workspace(1, 10, 10, 5, ctypes.byref(n)) == INVALID
+    assert lib.orthogonalize_workspace(1, 10, 10, 0, None) == INVALID
+
+
+def test_orthogonalize_refuses_host_tensors(lib):
+    import torch
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        pg.orthogonalize(torch.ones((4, 8)))
