@@ -157,6 +157,7 @@ constexpr unsigned int kErrFamilyF32CpAsyncMbar = 4;
 constexpr unsigned int kErrFamilyF32CpAsyncWs = 5;
 constexpr unsigned int kErrFamilyF32TmaWide = 6;
 constexpr unsigned int kErrFamilyOrthogonalize = 7;
+constexpr unsigned int kErrFamilyLayerNorm = 8;
 constexpr unsigned int kErrRoleConsumer = 1u << 8;
 constexpr unsigned int kErrRoleProducer = 2u << 8;
 constexpr unsigned int kErrRoleMma = 3u << 8;

@@ -9,39 +9,12 @@
 #include <cmath>
 #include <cstdint>
 
-#include "gemm_internal.h"
+#include "layer_norm_internal.h"
 #include "pipelined_train.h"
-#include "vector_io.cuh"
 
 namespace pg {
 
 namespace ln {
-
-struct Forward {
-    int rows, cols;
-    const void *x;
-    long long ldx;
-    const void *weight, *bias; // either may be null
-    int weight_bf16;
-    void *y;
-    long long ldy;
-    float *mean, *rstd; // both or neither
-    float eps;
-};
-
-struct Backward {
-    int rows, cols;
-    const void *dy, *x;
-    long long lddy, ldx;
-    const float *mean, *rstd;
-    const void *weight; // may be null
-    int weight_bf16;
-    void *dx;
-    long long lddx;
-    void *dweight, *dbias; // either may be null
-    float *partial;        // [parts][2][cols]: dweight's and dbias's partial sums
-    int parts;
-};
 
 // Sum over the CTA, the same value in every thread.  `scratch` holds 32
 // floats; the caller's next use of it comes after another barrier.
@@ -157,56 +130,156 @@ __global__ void __launch_bounds__(32 * kColumnRows) columns_kernel(const Backwar
     }
 }
 
-// dweight and dbias from the partial sums, in part order: 32 columns by 8
-// parts of threads, blockIdx.y choosing which of the two.
-__global__ void __launch_bounds__(256) finish_kernel(const Backward p)
+// dweight and dbias from the partial sums: 32 columns by 16 parts of threads,
+// blockIdx.y choosing which of the two.  Four loads of a thread in flight.
+constexpr int kFinishRows = 16;
+
+__global__ void __launch_bounds__(32 * kFinishRows) finish_kernel(const Backward p)
 {
-    __shared__ float s[8][32];
+    __shared__ float s[kFinishRows][32];
     const int j = blockIdx.x * 32 + threadIdx.x;
     const int which = blockIdx.y;
     void *out = which == 0 ? p.dweight : p.dbias;
+    grid_wait();
     if (!out)
         return;
-    float v = 0.0f;
-    if (j < p.cols)
-        for (int k = threadIdx.y; k < p.parts; k += 8)
-            v += p.partial[(static_cast<long long>(k) * 2 + which) * p.cols + j];
-    s[threadIdx.y][threadIdx.x] = v;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (j < p.cols) {
+        const float *from = p.partial + static_cast<long long>(which) * p.cols + j;
+        const long long pitch = 2ll * p.cols;
+        for (int k = threadIdx.y; k < p.parts; k += 4 * kFinishRows) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (k + u * kFinishRows < p.parts)
+                    v[u] += from[(k + u * kFinishRows) * pitch];
+        }
+    }
+    s[threadIdx.y][threadIdx.x] = (v[0] + v[1]) + (v[2] + v[3]);
     __syncthreads();
     if (threadIdx.y == 0 && j < p.cols) {
-        for (int k = 1; k < 8; ++k)
-            v += s[k][threadIdx.x];
-        store_f32(out, p.weight_bf16, j, v);
+        float t = s[0][threadIdx.x];
+        for (int k = 1; k < kFinishRows; ++k)
+            t += s[k][threadIdx.x];
+        store_f32(out, p.weight_bf16, j, t);
     }
 }
 
-// Runs of rows the column sums are cut into.
+// Most partial sums of a column that any variant makes.
 int backward_parts(int rows, int sms)
 {
     const int most = 2 * sms;
     return rows < most ? (rows < 1 ? 1 : rows) : most;
 }
 
-template <class T>
-int launch_forward(const Forward &p, cudaStream_t s)
+// Elements per thread `e`, rows at a time, and where they come from.  The
+// ring pays once a group has several rows to run ahead over; below that the
+// threads load their own.  `full`: there is a variant for rows without a rest.
+Plan spread(int rows, int cols, int e, int max_threads, int streams, int parameters, bool vectors, bool full,
+            size_t size, const Device &d)
 {
+    Plan plan = {};
+    const int tpr = (cols + e * 32 - 1) / (e * 32) * 32;
+    if (tpr > max_threads)
+        return plan;
+    plan.elements = e;
+    const int groups = std::max(1, std::min(max_threads / tpr, (rows + d.sms - 1) / d.sms));
+    const int trips = (rows + groups - 1) / groups;
+    const int row_bytes = cols * static_cast<int>(size);
+    const int slot_bytes = vectors ? row_bytes : (row_bytes + 15 + 15) / 16 * 16;
+    const int fixed = parameters * parameter_floats(cols) * 4;
+    const int layer = groups * streams * slot_bytes; // one slot of every group
+    const int slots = std::min({kMaxSlots, std::max(2, kRingBytes / layer), (kSmemBytes - fixed) / layer});
+    const bool ring = trips > 2 * d.sms && slots >= 2;
+    plan.source = !ring ? (vectors ? kVector : kScalar)
+                  : !vectors ? kRingScalar
+                  : cols == tpr * e && full ? kRingFull : kRingVector;
+    plan.shape = Shape{tpr, groups, slots, slot_bytes, d.status, call_wait_limit_ns(), call_withhold()};
+    plan.grid = std::min(trips, d.sms);
+    plan.smem = ring ? fixed + slots * groups * streams * slot_bytes : 0;
+    return plan;
+}
+
+bool vector_rows(const void *p, long long ld, int rows, size_t size)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows <= 1 || (ld * static_cast<long long>(size)) % 16 == 0);
+}
+
+bool vector_parameter(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+template <class T>
+int launch_forward(const Forward &p, const Device &d, cudaStream_t s)
+{
+    constexpr bool kBf16 = sizeof(T) == 2;
+    const bool vectors = p.cols % Vec16<T>::kElements == 0 && vector_rows(p.x, p.ldx, p.rows, sizeof(T)) &&
+                         vector_rows(p.y, p.ldy, p.rows, sizeof(T)) && vector_parameter(p.weight) &&
+                         vector_parameter(p.bias);
+    // 16 elements a thread give a single row the most threads; 32 give many
+    // rows the most groups, whose reductions overlap.
+    const int e = p.cols <= 512 || ((p.rows <= 2 * d.sms || !vectors) && p.cols <= 8192) ? 16 : 32;
+    Plan plan = spread(p.rows, p.cols, e, forward_threads(e), 1, 2, vectors, true, sizeof(T), d);
+    if (plan.elements != 0) {
+        if (!from_ring(plan.source)) // no ring to keep the memory system busy: every CTA that fits
+            plan.grid = std::min((p.rows + plan.shape.groups - 1) / plan.shape.groups, 4 * d.sms);
+        return launch_forward_rows(p, kBf16, plan, d, s);
+    }
     const int grid = p.rows < 65536 ? p.rows : 65536;
     forward_any_kernel<T><<<grid, kAnyThreads, 0, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
-template <class T>
-int launch_backward(const Backward &p, cudaStream_t s)
+int launch_finish(const Backward &p, bool overlap, cudaStream_t s)
 {
-    const unsigned column_blocks = static_cast<unsigned>((p.cols + 31) / 32);
-    if (p.dweight || p.dbias) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((p.cols + 31) / 32), 2);
+    cfg.blockDim = dim3(32, kFinishRows);
+    cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, finish_kernel, p) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+template <class T>
+int launch_backward(Backward p, const Device &d, cudaStream_t s)
+{
+    constexpr bool kBf16 = sizeof(T) == 2;
+    const bool columns = p.dweight || p.dbias;
+    const bool vectors = p.cols % Vec16<T>::kElements == 0 && vector_rows(p.x, p.ldx, p.rows, sizeof(T)) &&
+                         vector_rows(p.dy, p.lddy, p.rows, sizeof(T)) && vector_rows(p.dx, p.lddx, p.rows, sizeof(T)) &&
+                         vector_parameter(p.weight);
+    // 16 elements leave room for the two column sums of each in registers.
+    const int e = p.cols <= 8192 ? 16 : 32;
+    Plan plan = spread(p.rows, p.cols, e, kBackwardThreads, 2, 1, vectors, e == 16, sizeof(T), d);
+    if (plan.elements != 0 && p.rows > 0) {
+        p.parts = plan.grid;
+        const int st = launch_backward_rows(p, kBf16, plan, d, s);
+        return st != GEMM_OK || !columns || p.parts == 1 ? st : launch_finish(p, true, s);
+    }
+    if (columns) {
+        const unsigned column_blocks = static_cast<unsigned>((p.cols + 31) / 32);
         columns_kernel<T><<<dim3(column_blocks, p.parts), dim3(32, kColumnRows), 0, s>>>(p);
-        finish_kernel<<<dim3(column_blocks, 2), dim3(32, 8), 0, s>>>(p);
+        const int st = launch_finish(p, false, s);
+        if (st != GEMM_OK)
+            return st;
     }
     const int grid = p.rows < 65536 ? p.rows : 65536;
     if (grid > 0)
         backward_any_kernel<T><<<grid, kAnyThreads, 0, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+// The current device, and what its kernels need to know.
+int enter(Device *d)
+{
+    const int st = device_checked(&d->index);
+    if (st != GEMM_OK)
+        return st;
+    d->sms = device_sms();
+    d->ctx = current_context_id();
+    d->status = device_status_word(d->index, d->ctx);
+    return d->status ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
 bool valid_dtype(int d) { return d == GEMM_DTYPE_F32 || d == GEMM_DTYPE_BF16; }
@@ -239,15 +312,15 @@ int layer_norm(int rows, int cols, const void *x, long long ldx, int dtype, cons
         !ln::aligned_to(bias, weight_dtype) || !ln::aligned_to(mean, GEMM_DTYPE_F32) ||
         !ln::aligned_to(rstd, GEMM_DTYPE_F32))
         return GEMM_ERR_MISALIGNED;
-    int dev;
-    const int st = device_checked(&dev);
+    ln::Device d;
+    const int st = ln::enter(&d);
     if (st != GEMM_OK)
         return st;
     if (rows == 0)
         return GEMM_OK;
     const ln::Forward p{rows, cols, x, ldx, weight, bias, weight_dtype == GEMM_DTYPE_BF16, y, ldy, mean, rstd, eps};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return dtype == GEMM_DTYPE_F32 ? ln::launch_forward<float>(p, s) : ln::launch_forward<__nv_bfloat16>(p, s);
+    return dtype == GEMM_DTYPE_F32 ? ln::launch_forward<float>(p, d, s) : ln::launch_forward<__nv_bfloat16>(p, d, s);
 }
 
 int layer_norm_backward_workspace(int rows, int cols, size_t *bytes)
@@ -279,14 +352,14 @@ int layer_norm_backward(int rows, int cols, const void *dy, long long lddy, cons
     (void)layer_norm_backward_workspace(rows, cols, &need);
     if (columns && (!workspace || workspace_bytes < need))
         return GEMM_ERR_INVALID_ARG;
-    int dev;
-    const int st = device_checked(&dev);
+    ln::Device d;
+    const int st = ln::enter(&d);
     if (st != GEMM_OK)
         return st;
-    ln::Backward p{rows, cols, dy, x, lddy, ldx, mean, rstd, weight, weight_dtype == GEMM_DTYPE_BF16, dx, lddx,
-                   dweight, dbias, static_cast<float *>(workspace), ln::backward_parts(rows, device_sms())};
+    const ln::Backward p{rows, cols, dy, x, lddy, ldx, mean, rstd, weight, weight_dtype == GEMM_DTYPE_BF16, dx, lddx,
+                   dweight, dbias, static_cast<float *>(workspace), ln::backward_parts(rows, d.sms)};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return dtype == GEMM_DTYPE_F32 ? ln::launch_backward<float>(p, s) : ln::launch_backward<__nv_bfloat16>(p, s);
+    return dtype == GEMM_DTYPE_F32 ? ln::launch_backward<float>(p, d, s) : ln::launch_backward<__nv_bfloat16>(p, d, s);
 }
 
 } // extern "C"

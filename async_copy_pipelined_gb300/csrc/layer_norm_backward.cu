@@ -1,0 +1,240 @@
+// Gradient of layer norm for rows that a group of threads holds in registers:
+// dy and x are read once and dx written once, and each thread sums dweight and
+// dbias of its columns over all its rows in registers.  What remains of those
+// is one partial sum per column and CTA, added up by a second small kernel.
+#include "layer_norm_internal.h"
+
+namespace pg {
+
+namespace ln {
+
+template <class T, int E, Source S>
+__global__ void __launch_bounds__(kBackwardThreads, 1) backward_rows_kernel(const Backward p, const Shape shape)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[kMaxWarps * kMaxSlots];
+    __shared__ GroupScratch scratch;
+    constexpr bool kRing = from_ring(S);
+    // Up to 16 elements a thread keeps a row's between its two passes; with
+    // 32 the column sums take those registers, and the second pass reads the
+    // row again where it is.
+    constexpr bool kKeep = E <= 16;
+    grid_launch_next(); // the kernel that adds the partial sums waits for this one's end
+    Group g(threadIdx.x, shape.tpr, &scratch);
+    using Columns = Spread<T, E, S>;
+    const Columns at(g.t, p.cols);
+    constexpr int kPiece = Columns::kPiece, kPieces = Columns::kPieces;
+    float *weight = reinterpret_cast<float *>(smem);
+    uint8_t *slots = smem + (kRing ? parameter_floats(p.cols) * 4 : 0);
+    Ring<2> ring(smem_u32(bars), smem_u32(slots), shape, g, p.cols * static_cast<int>(sizeof(T)), p.rows);
+    const uint8_t *own = slots + (ring.slots_at - smem_u32(slots));
+    if constexpr (kRing) {
+        ring.in[0] = Stream{static_cast<const uint8_t *>(p.x), p.ldx * static_cast<long long>(sizeof(T))};
+        ring.in[1] = Stream{static_cast<const uint8_t *>(p.dy), p.lddy * static_cast<long long>(sizeof(T))};
+        ring.init();
+        ring.start(); // a thread's own copies on its own mbarriers; the others meet them past the barrier
+        at.copy_parameter(weight, p.weight, p.weight_bf16, 1.0f, p.cols);
+    }
+    __syncthreads();
+    unsigned long long dw[E / 2], db[E / 2];
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i)
+        dw[i] = db[i] = 0ull;
+    const float inv = -1.0f / static_cast<float>(p.cols);
+    auto weight_piece = [&](int k, float *v) {
+        if constexpr (kRing)
+            at.load_copy_piece(weight, p.cols, k, v);
+        else
+            at.load_parameter_piece(p.weight, p.weight_bf16, 1.0f, k, v);
+    };
+
+    const long long step = static_cast<long long>(gridDim.x) * shape.groups;
+    const long long first = static_cast<long long>(blockIdx.x) * shape.groups + g.index;
+    float next_mean = 0.0f, next_rstd = 0.0f; // loaded a row ahead
+    if (first < p.rows) {
+        next_mean = p.mean[first];
+        next_rstd = p.rstd[first];
+    }
+    // The bound is the same in the whole group.
+    for (long long row = first; row < p.rows; row += step) {
+        const float mean = next_mean, rstd = next_rstd;
+        if (row + step < p.rows) {
+            next_mean = p.mean[row + step];
+            next_rstd = p.rstd[row + step];
+        }
+        Row<T> x, dy;
+        if constexpr (kRing) {
+            ring.wait();
+            x = ring.template view<T>(own, 0, row);
+            dy = ring.template view<T>(own, 1, row);
+        } else {
+            x.near = static_cast<const T *>(p.x) + row * p.ldx;
+            dy.near = static_cast<const T *>(p.dy) + row * p.lddy;
+        }
+        T *dx = static_cast<T *>(p.dx) + row * p.lddx;
+        const unsigned long long minus = pair(-mean, -mean), scale = pair(rstd, rstd);
+        // Two chains of paired additions for each sum.
+        unsigned long long s1[2] = {0ull, 0ull}, s2[2] = {0ull, 0ull};
+        // xhat and t = dy weight of pairs 2j, 2j + 1 of the thread, added to
+        // the row's and the columns' sums.  Absent elements: dy and so t are 0.
+        auto first_pass = [&](int j, unsigned long long xv, unsigned long long gv, unsigned long long wv,
+                              unsigned long long &xhat, unsigned long long &t) {
+            xhat = mul2(add2(xv, minus), scale);
+            t = mul2(gv, wv);
+            s1[j & 1] = add2(s1[j & 1], t);
+            s2[j & 1] = fma2(t, xhat, s2[j & 1]);
+            dw[j] = fma2(gv, xhat, dw[j]);
+            db[j] = add2(db[j], gv);
+        };
+        if constexpr (kKeep) {
+            unsigned long long xhat[E / 2], t[E / 2];
+            {
+                float xv[E], gv[E], wv[E];
+                at.load(x, xv);
+                at.load(dy, gv);
+#pragma unroll
+                for (int k = 0; k < kPieces; ++k)
+                    weight_piece(k, wv + k * kPiece);
+#pragma unroll
+                for (int j = 0; j < E / 2; ++j)
+                    first_pass(j, pair(xv[2 * j], xv[2 * j + 1]), pair(gv[2 * j], gv[2 * j + 1]),
+                               pair(wv[2 * j], wv[2 * j + 1]), xhat[j], t[j]);
+            }
+            const float2 c = g.sum(both(add2(s1[0], s1[1])), both(add2(s2[0], s2[1])));
+            if constexpr (kRing) // the group has met in the sum, past its loads
+                ring.next();
+            const float c1 = c.x * inv, c2 = c.y * inv; // negated means
+            const unsigned long long m1 = pair(c1, c1), m2 = pair(c2, c2);
+            float v[E];
+#pragma unroll
+            for (int j = 0; j < E / 2; ++j)
+                split(mul2(add2(fma2(xhat[j], m2, t[j]), m1), scale), v[2 * j], v[2 * j + 1]);
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k)
+                at.store_piece(dx, k, v + k * kPiece);
+        } else {
+            constexpr int kStep = kPiece == 1 ? 2 : kPiece; // elements at a time: whole pairs
+            auto load = [&](int i, float (&xv)[kStep], float (&gv)[kStep], float (&wv)[kStep]) {
+#pragma unroll
+                for (int e = 0; e < kStep; e += kPiece) {
+                    const int k = (i + e) / kPiece;
+                    at.load_piece(x, k, xv + e);
+                    at.load_piece(dy, k, gv + e);
+                    weight_piece(k, wv + e);
+                }
+            };
+#pragma unroll
+            for (int i = 0; i < E; i += kStep) {
+                float xv[kStep], gv[kStep], wv[kStep];
+                load(i, xv, gv, wv);
+#pragma unroll
+                for (int e = 0; e < kStep; e += 2) {
+                    unsigned long long xhat, t;
+                    first_pass((i + e) / 2, pair(xv[e], xv[e + 1]), pair(gv[e], gv[e + 1]), pair(wv[e], wv[e + 1]),
+                               xhat, t);
+                }
+            }
+            const float2 c = g.sum(both(add2(s1[0], s1[1])), both(add2(s2[0], s2[1])));
+            const float c1 = c.x * inv, c2 = c.y * inv; // negated means
+            const unsigned long long m1 = pair(c1, c1), m2 = pair(c2, c2);
+#pragma unroll
+            for (int i = 0; i < E; i += kStep) {
+                float xv[kStep], gv[kStep], wv[kStep], v[kStep];
+                load(i, xv, gv, wv);
+#pragma unroll
+                for (int e = 0; e < kStep; e += 2) {
+                    const unsigned long long xhat = mul2(add2(pair(xv[e], xv[e + 1]), minus), scale);
+                    const unsigned long long t = mul2(pair(gv[e], gv[e + 1]), pair(wv[e], wv[e + 1]));
+                    split(mul2(add2(fma2(xhat, m2, t), m1), scale), v[e], v[e + 1]);
+                }
+#pragma unroll
+                for (int e = 0; e < kStep; e += kPiece)
+                    at.store_piece(dx, (i + e) / kPiece, v + e);
+            }
+            if constexpr (kRing) {
+                g.barrier();
+                ring.next();
+            }
+        }
+    }
+    if constexpr (kRing)
+        ring.drain();
+
+    if (!p.dweight && !p.dbias)
+        return;
+    // The groups' sums in group order, through shared memory (the ring's: all
+    // of its rows have been taken); the last group has the CTA's.
+    float *total = reinterpret_cast<float *>(smem); // [2][cols]
+    for (int k = 0; k < shape.groups; ++k) {
+        if (shape.groups > 1)
+            __syncthreads();
+        if (g.index != k)
+            continue;
+        const bool last = k == shape.groups - 1;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            if (!at.has(i / kPiece))
+                break;
+            const int j = at.column(i / kPiece) + i % kPiece;
+            float lo, hi;
+            split(dw[i / 2], lo, hi);
+            float vw = i & 1 ? hi : lo;
+            split(db[i / 2], lo, hi);
+            float vb = i & 1 ? hi : lo;
+            if (k > 0) {
+                vw += total[j];
+                vb += total[p.cols + j];
+            }
+            if (!last) {
+                total[j] = vw;
+                total[p.cols + j] = vb;
+            } else if (gridDim.x == 1) {
+                if (p.dweight)
+                    store_f32(p.dweight, p.weight_bf16, j, vw);
+                if (p.dbias)
+                    store_f32(p.dbias, p.weight_bf16, j, vb);
+            } else {
+                float *out = p.partial + static_cast<long long>(blockIdx.x) * 2 * p.cols;
+                out[j] = vw;
+                out[p.cols + j] = vb;
+            }
+        }
+    }
+}
+
+template <class T, int E, Source S>
+static int launch(const Backward &p, const Plan &plan, const Device &d, cudaStream_t s)
+{
+    const int sums = plan.shape.groups > 1 ? 2 * p.cols * 4 : 0; // the groups' column sums
+    static std::atomic<unsigned long long> limit_set[kMaxDevices];
+    if (ensure_smem_limit(backward_rows_kernel<T, E, S>, kSmemBytes, d.index, d.ctx, limit_set) != GEMM_OK)
+        return GEMM_ERR_CUDA;
+    const int threads = plan.shape.groups * plan.shape.tpr;
+    backward_rows_kernel<T, E, S><<<plan.grid, threads, std::max(plan.smem, sums), s>>>(p, plan.shape);
+    return cudaGetLastError() == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+template <class T, int E>
+static int launch_source(const Backward &p, const Plan &plan, const Device &d, cudaStream_t s)
+{
+    if constexpr (E == 16)
+        if (plan.source == kRingFull)
+            return launch<T, E, kRingFull>(p, plan, d, s);
+    switch (plan.source) {
+    case kRingVector: return launch<T, E, kRingVector>(p, plan, d, s);
+    case kRingScalar: return launch<T, E, kRingScalar>(p, plan, d, s);
+    case kVector: return launch<T, E, kVector>(p, plan, d, s);
+    default: return launch<T, E, kScalar>(p, plan, d, s);
+    }
+}
+
+int launch_backward_rows(const Backward &p, bool bf16, const Plan &plan, const Device &d, cudaStream_t s)
+{
+    if (plan.elements == 16)
+        return bf16 ? launch_source<__nv_bfloat16, 16>(p, plan, d, s) : launch_source<float, 16>(p, plan, d, s);
+    return bf16 ? launch_source<__nv_bfloat16, 32>(p, plan, d, s) : launch_source<float, 32>(p, plan, d, s);
+}
+
+} // namespace ln
+
+} // namespace pg

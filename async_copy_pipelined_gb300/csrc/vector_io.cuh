@@ -30,4 +30,48 @@ __device__ __forceinline__ void store_f32(void *base, bool bf16, long long j, fl
         static_cast<float *>(base)[j] = v;
 }
 
+// Sixteen bytes as float32 values, and back.
+template <class T>
+struct Vec16;
+
+template <>
+struct Vec16<float> {
+    static constexpr int kElements = 4;
+    static __device__ __forceinline__ void unpack(const uint4 &q, float *v)
+    {
+        v[0] = __uint_as_float(q.x);
+        v[1] = __uint_as_float(q.y);
+        v[2] = __uint_as_float(q.z);
+        v[3] = __uint_as_float(q.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float *v)
+    {
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    }
+};
+
+template <>
+struct Vec16<__nv_bfloat16> {
+    static constexpr int kElements = 8;
+    static __device__ __forceinline__ void unpack(const uint4 &q, float *v)
+    {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(w[e] << 16);
+            v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float *v)
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
 } // namespace pg

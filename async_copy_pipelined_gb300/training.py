@@ -37,46 +37,53 @@ def bind(l):
     return l
 
 
+_torch = None
+_CODES = {}
+
+
+def _load():
+    """torch, on the first call: importing this package does not import it."""
+    global _torch
+    if _torch is None:
+        import torch
+        _CODES[torch.float32] = F32
+        _CODES[torch.bfloat16] = BF16
+        _torch = torch
+    return _torch
+
+
 def _dtype(t, name):
-    import torch
-    if t.dtype == torch.float32:
-        return F32
-    if t.dtype == torch.bfloat16:
-        return BF16
-    raise TypeError(f"{name} must be float32 or bfloat16, not {t.dtype}")
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, not {t.dtype}")
+    return code
 
 
 def _rows(t, name):
     """(rows, cols, pitch) of a tensor seen as rows of its last dimension:
     the rows' elements contiguous, the rows at one common distance."""
-    if t.dim() == 0:
+    shape = t.shape
+    if len(shape) == 0:
         raise ValueError(f"{name} needs at least one dimension")
-    cols = t.shape[-1]
+    cols = shape[-1]
     if cols < 1:
         raise ValueError(f"{name} has empty rows")
-    if t.dim() == 1:
-        rows, pitch = 1, cols
-    elif t.dim() == 2:
-        rows, pitch = t.shape[0], t.stride(0)
-    else:
-        rows = t.numel() // cols
-        pitch = t.stride(-2)
-        if rows > 0:
-            step = pitch * t.shape[-2]
-            for d in range(t.dim() - 3, -1, -1):
-                if t.shape[d] != 1:
-                    if t.shape[-2] == 1 and step == pitch:
-                        pitch = step = t.stride(d)  # the rows' distance is this dimension's
-                    elif t.stride(d) != step:
-                        raise ValueError(f"the rows of {name} must lie at one common distance")
-                    step = t.stride(d) * t.shape[d]
-    if rows == 0:
-        return 0, cols, cols
-    if cols > 1 and t.stride(-1) != 1:
+    if t.is_contiguous():
+        return t.numel() // cols, cols, cols
+    stride = t.stride()
+    if cols > 1 and stride[-1] != 1:
         raise ValueError(f"{name} must have unit column stride (row-major rows)")
-    if rows == 1:
-        pitch = cols
-    elif pitch < cols:
+    rows, pitch, step = 1, cols, None  # step: the distance the next dimension out must have
+    for n, d in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+        if n == 1:
+            continue
+        if step is None:
+            pitch = d
+        elif d != step:
+            raise ValueError(f"the rows of {name} must lie at one common distance")
+        rows *= n
+        step = d * n
+    if rows > 1 and pitch < cols:
         raise ValueError(f"the rows of {name} overlap in memory")
     return rows, cols, pitch
 
@@ -107,9 +114,9 @@ def _refuse_overlap(out, out_rows, t, t_rows, name, what):
 
 
 def _enter(device, stream):
-    """The launch stream's handle, and whether it is another than the
-    device's current one (whose allocator order then has to be kept)."""
-    import torch
+    """The launch stream's handle, and the stream itself where it is another
+    than the device's current one (whose allocator order has to be kept)."""
+    torch = _torch
     if device.type != "cuda":
         raise ValueError("operands must be CUDA tensors")
     cur = torch.cuda.current_stream(device)
@@ -137,21 +144,24 @@ def _record(other, *tensors):
                 t.record_stream(other)
 
 
-def _on(device):
-    """The context in which the library is called: `device` current."""
-    import contextlib
-    import torch
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _call(device, what, fn, *args):
+    """A library call with `device` current, and its status checked."""
+    if _torch.cuda.current_device() == device.index:
+        st = fn(*args)
+    else:
+        with _torch.cuda.device(device):
+            st = fn(*args)
+    if st != _pg.GEMM_OK:
+        raise _pg.GemmError(st, what)
 
 
 def _workspace(kind, device, handle, nbytes, other):
     """A buffer kept per operator, device and stream, grown as needed: calls
     on one stream never overlap."""
-    import torch
     key = (kind, device.index, handle)
     buf = _workspaces.get(key)
     if buf is None or buf.numel() < nbytes:
-        buf = _workspaces[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        buf = _workspaces[key] = _torch.empty(nbytes, dtype=_torch.uint8, device=device)
     _record(other, buf)
     return buf
 
@@ -167,7 +177,7 @@ def layer_norm(x, weight=None, bias=None, out=None, *, eps=1e-5, stats=False, st
 
     stats: return (y, mean, rstd) with the rows' float32 statistics, which
     layer_norm_backward takes; otherwise y alone."""
-    import torch
+    torch = _load()
     dt = _dtype(x, "x")
     rows = _rows(x, "x")
     device = x.device
@@ -182,7 +192,7 @@ def layer_norm(x, weight=None, bias=None, out=None, *, eps=1e-5, stats=False, st
         wdt = _dtype(bias, "bias")
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=device)
-        out_rows = (rows[0], rows[1], rows[1])
+        ldy = rows[1]
     else:
         if out.device != device:
             raise ValueError(f"out is on {out.device}, x on {device}: all operands must be on one device")
@@ -190,16 +200,16 @@ def layer_norm(x, weight=None, bias=None, out=None, *, eps=1e-5, stats=False, st
             raise ValueError("out must have x's shape and type")
         out_rows = _rows(out, "out")
         _refuse_overlap(out, out_rows, x, rows, "x", "out")
-    mean = rstd = None
+        ldy = out_rows[2]
+    mean = rstd = pm = pr = None
     if stats:
-        both = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=device)
-        mean, rstd = both[0], both[1]
-    with _on(device):
-        st = _pg.lib().layer_norm(rows[0], rows[1], x.data_ptr(), rows[2], dt, pw, pb, wdt, out.data_ptr(),
-                                  out_rows[2], mean.data_ptr() if stats else None, rstd.data_ptr() if stats else None,
-                                  eps, handle)
-    _pg._check(st, "layer_norm")
-    _record(other, x, weight, bias, out, mean)
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
+        pm, pr = mean.data_ptr(), rstd.data_ptr()
+    _call(device, "layer_norm", _pg.lib().layer_norm, rows[0], rows[1], x.data_ptr(), rows[2], dt, pw, pb, wdt,
+          out.data_ptr(), ldy, pm, pr, eps, handle)
+    if other is not None:
+        _record(other, x, weight, bias, out, mean, rstd)
     return (out, mean, rstd) if stats else out
 
 
@@ -211,7 +221,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, *, stream=None
     weight is None.  All sums are float32 in an order fixed by the sizes: the
     same inputs give the same bits.  out: where dx goes (dy or x itself for an
     in-place call); allocated if None."""
-    import torch
+    torch = _load()
     dt = _dtype(x, "x")
     rows = _rows(x, "x")
     device = x.device
@@ -227,11 +237,9 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, *, stream=None
         if t.dtype != torch.float32 or t.numel() != rows[0] or not t.is_contiguous():
             raise ValueError(f"{name} must be {rows[0]} contiguous float32 values")
     pw = _vector(weight, "weight", rows[1], device)
-    wdt = F32
-    dweight = dbias = ws = None
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=device)
-        out_rows = (rows[0], rows[1], rows[1])
+        lddx = rows[1]
     else:
         if out.device != device:
             raise ValueError(f"out is on {out.device}, x on {device}: all operands must be on one device")
@@ -240,24 +248,25 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, *, stream=None
         out_rows = _rows(out, "out")
         _refuse_overlap(out, out_rows, x, rows, "x", "out")
         _refuse_overlap(out, out_rows, dy, dy_rows, "dy", "out")
+        lddx = out_rows[2]
     l = _pg.lib()
-    with _on(device):
-        if weight is not None:
-            wdt = _dtype(weight, "weight")
-            both = torch.empty((2, rows[1]), dtype=weight.dtype, device=device)
-            dweight, dbias = both[0], both[1]
-            need = ctypes.c_size_t()
-            _pg._check(l.layer_norm_backward_workspace(rows[0], rows[1], ctypes.byref(need)),
-                       "layer_norm_backward_workspace")
-            ws = _workspace("layer_norm_backward", device, handle, need.value, other)
-        st = l.layer_norm_backward(rows[0], rows[1], dy.data_ptr(), dy_rows[2], x.data_ptr(), rows[2], dt,
-                                   mean.data_ptr(), rstd.data_ptr(), pw, wdt, out.data_ptr(), out_rows[2],
-                                   dweight.data_ptr() if ws is not None else None,
-                                   dbias.data_ptr() if ws is not None else None,
-                                   ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
-                                   handle)
-    _pg._check(st, "layer_norm_backward")
-    _record(other, dy, x, mean, rstd, weight, out, dweight)
+    wdt, ws_bytes = F32, 0
+    dweight = dbias = ws = pdw = pdb = pws = None
+    if weight is not None:
+        wdt = _dtype(weight, "weight")
+        dweight = torch.empty(rows[1], dtype=weight.dtype, device=device)
+        dbias = torch.empty(rows[1], dtype=weight.dtype, device=device)
+        need = ctypes.c_size_t()
+        _call(device, "layer_norm_backward_workspace", l.layer_norm_backward_workspace, rows[0], rows[1],
+              ctypes.byref(need))
+        ws = _workspace("layer_norm_backward", device, handle, need.value, other)
+        ws_bytes = ws.numel()
+        pdw, pdb, pws = dweight.data_ptr(), dbias.data_ptr(), ws.data_ptr()
+    _call(device, "layer_norm_backward", l.layer_norm_backward, rows[0], rows[1], dy.data_ptr(), dy_rows[2],
+          x.data_ptr(), rows[2], dt, mean.data_ptr(), rstd.data_ptr(), pw, wdt, out.data_ptr(), lddx, pdw, pdb, pws,
+          ws_bytes, handle)
+    if other is not None:
+        _record(other, dy, x, mean, rstd, weight, out, dweight, dbias)
     return out, dweight, dbias
 
 
@@ -298,7 +307,7 @@ def orthogonalize(G, out=None, *, steps=5, coefficients=COEFFICIENTS, eps=1e-7, 
     where the result goes (G itself for an in-place call).  workspace: "auto"
     keeps one buffer per device and stream, grown as needed; or a uint8 CUDA
     tensor of at least orthogonalize_workspace() bytes (the C header)."""
-    import torch
+    torch = _load()
     dt = _dtype(G, "G")
     batch, m, n, ldg, g_batch = _matrices(G, "G")
     device = G.device
@@ -321,20 +330,19 @@ def orthogonalize(G, out=None, *, steps=5, coefficients=COEFFICIENTS, eps=1e-7, 
     if len(triples) != 3 * steps or steps < 1:
         raise ValueError("coefficients must be one (a, b, c), or one for each of one or more steps")
     l = _pg.lib()
-    with _on(device):
-        need = ctypes.c_size_t()
-        _pg._check(l.orthogonalize_workspace(batch, m, n, odt, ctypes.byref(need)), "orthogonalize_workspace")
-        if isinstance(workspace, str):
-            if workspace != "auto":
-                raise ValueError('workspace must be "auto" or a uint8 CUDA tensor')
-            ws = _workspace("orthogonalize", device, handle, need.value, other)
-        else:
-            ws = workspace
-            if ws.device != device:
-                raise ValueError(f"workspace is on {ws.device}, G on {device}")
-        st = l.orthogonalize(batch, m, n, G.data_ptr(), ldg, g_batch, dt, out.data_ptr(), ldo, o_batch, odt, steps,
-                             (ctypes.c_float * len(triples))(*triples), eps, ws.data_ptr(),
-                             ws.numel() * ws.element_size(), handle)
-    _pg._check(st, "orthogonalize")
-    _record(other, G, out, ws)
+    need = ctypes.c_size_t()
+    _call(device, "orthogonalize_workspace", l.orthogonalize_workspace, batch, m, n, odt, ctypes.byref(need))
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError('workspace must be "auto" or a uint8 CUDA tensor')
+        ws = _workspace("orthogonalize", device, handle, need.value, other)
+    else:
+        ws = workspace
+        if ws.device != device:
+            raise ValueError(f"workspace is on {ws.device}, G on {device}")
+    _call(device, "orthogonalize", l.orthogonalize, batch, m, n, G.data_ptr(), ldg, g_batch, dt, out.data_ptr(), ldo,
+          o_batch, odt, steps, (ctypes.c_float * len(triples))(*triples), eps, ws.data_ptr(),
+          ws.numel() * ws.element_size(), handle)
+    if other is not None:
+        _record(other, G, out, ws)
     return out
