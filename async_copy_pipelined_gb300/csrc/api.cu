@@ -227,24 +227,25 @@ int encode_tensor_map_2d(void *map_out, int dtype_is_bf16, const void *base, uin
     return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
-int encode_tensor_map_3d(void *map_out, TensorElement element, const void *base, uint64_t cols, uint64_t rows,
-                         uint64_t planes, uint64_t row_pitch, uint64_t plane_pitch, uint32_t box_cols,
-                         uint32_t box_rows, bool swizzle_128b)
+int encode_tensor_map(void *map_out, TensorElement element, const void *base, int rank, const uint64_t *dims,
+                      const uint64_t *pitches, const uint32_t *box, int swizzle_bytes)
 {
-    if ((reinterpret_cast<uintptr_t>(base) & 15u) != 0 || (row_pitch & 15u) != 0 || (plane_pitch & 15u) != 0)
+    uint64_t low = reinterpret_cast<uintptr_t>(base);
+    for (int k = 0; k < rank - 1; ++k)
+        low |= pitches[k];
+    if ((low & 15u) != 0)
         return GEMM_ERR_MISALIGNED;
     PFN_cuTensorMapEncodeTiled_v12000 encode = get_encode_fn();
     if (!encode)
         return GEMM_ERR_CUDA;
-    const cuuint64_t dims[3] = {cols, rows, planes};
-    const cuuint64_t strides[2] = {row_pitch, plane_pitch};
-    const cuuint32_t box[3] = {box_cols, box_rows, 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     const CUresult r = encode(static_cast<CUtensorMap *>(map_out),
                               element == kElement16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                              3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              swizzle_128b ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                              rank, const_cast<void *>(base), dims, pitches, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              swizzle_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                              : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                    : CU_TENSOR_MAP_SWIZZLE_NONE,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
 }

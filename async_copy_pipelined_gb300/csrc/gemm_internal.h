@@ -137,13 +137,13 @@ unsigned int *device_status_word(int dev, unsigned long long ctx);
 int encode_tensor_map_2d(void *map_out, int dtype_is_bf16, const void *base, uint64_t cols, uint64_t rows,
                          uint64_t pitch_bytes, uint32_t box_cols, uint32_t box_rows, int swizzle_128b);
 
-// A 3-D tiled tensor map over 2-byte floating elements (float16 or bfloat16:
-// the copies move bits, and an element outside is zero in both) or float32
-// ones: `planes` matrices of rows x cols, pitches in bytes.
+// A tiled tensor map of three or four dimensions over 2-byte floating elements
+// (float16 or bfloat16: the copies move bits, and an element outside is zero
+// in both) or float32 ones.  pitches: bytes of one step in dimensions 1 ...
+// swizzle_bytes: 0, 64 or 128.
 enum TensorElement { kElement16, kElement32 };
-int encode_tensor_map_3d(void *map_out, TensorElement element, const void *base, uint64_t cols, uint64_t rows,
-                         uint64_t planes, uint64_t row_pitch, uint64_t plane_pitch, uint32_t box_cols,
-                         uint32_t box_rows, bool swizzle_128b);
+int encode_tensor_map(void *map_out, TensorElement element, const void *base, int rank, const uint64_t *dims,
+                      const uint64_t *pitches, const uint32_t *box, int swizzle_bytes);
 
 // This call's wait limit and withheld ring position (test hooks included).
 unsigned long long call_wait_limit_ns();

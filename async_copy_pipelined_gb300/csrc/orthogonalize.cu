@@ -61,8 +61,7 @@ namespace orth {
 constexpr int BK = 64;                          // K block: 128 bytes of float16
 constexpr int kUmmaM = 128;
 constexpr int kUmmaK = 16;
-constexpr int kBox = 64;                        // every load is a 64 x 64 box
-constexpr uint32_t kBoxBytes = kBox * kBox * 2; // 8 KiB
+constexpr uint32_t kAtomBytes = 64 * BK * 2;    // 64 columns of an MN-major operand: 8 KiB
 constexpr int kDiagBlock = 256;                 // side of the diagonal blocks that keep the extra plane
 constexpr uint32_t kStagingBytes = 32 * 128;    // per epilogue warp: 32 rows of 128 bytes
 
@@ -93,7 +92,10 @@ constexpr int kMaxPasses = 6;
 enum Output { kPlanes, kBf16, kF32 };
 
 struct Maps {
-    CUtensorMap left, left_diag, right, right_diag; // 64 x 64 boxes, 128-byte swizzle
+    // Loads, one box per operand and K block, 128-byte swizzle: 64 k by the
+    // tile's rows, or for Q X's right operand its columns in groups of 64 by
+    // 64 k.
+    CUtensorMap left, left_diag, right, right_diag;
     CUtensorMap store, mirror, store_diag, mirror_diag;
 };
 
@@ -228,16 +230,30 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t w)
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
-// One epilogue warp's 4 KiB staging buffer, from which a TMA store moves a
-// box.  Each write waits until the store before it has read the buffer.
-struct Staging {
-    uint32_t addr;
-    int lane;
+// An epilogue warp's 4 KiB staging buffers, from which TMA stores move boxes.
+// The one of its own is written again when the store before has read it.  In
+// a CTA's last tile the ring is idle and lends each warp kLentBufs more, so
+// that no write waits.
+constexpr int kLentBufs = 4;
 
-    __device__ __forceinline__ void begin() const
+struct Staging {
+    uint32_t own, lent; // first addresses; lent 0: not now
+    int lane;
+    uint32_t addr = 0;
+    int turn = 0;
+
+    __device__ __forceinline__ void begin()
     {
-        if (lane == 0)
-            bulk_wait_group_read<0>();
+        if (lent == 0) {
+            addr = own;
+            if (lane == 0)
+                bulk_wait_group_read<0>();
+        } else {
+            addr = lent + static_cast<uint32_t>(turn) * kStagingBytes;
+            turn = turn + 1 == kLentBufs ? 0 : turn + 1;
+            if (lane == 0)
+                bulk_wait_group_read<kLentBufs - 1>();
+        }
         __syncwarp();
     }
     __device__ __forceinline__ void end(const CUtensorMap *map, int x, int y, int z) const
@@ -259,15 +275,28 @@ struct Staging {
                          "r"(w[4 * j]), "r"(w[4 * j + 1]), "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
                          : "memory");
     }
-    // The transpose: 64 rows of 32 two-byte elements, this lane's column.
-    __device__ __forceinline__ void column16(const uint32_t (&w)[32]) const
+    // The transpose of what row() has put into this buffer, 64 rows of 32
+    // two-byte elements, in 8 x 8 blocks: taken to registers, and (after
+    // begin()) put down in the 64-byte swizzle.
+    __device__ __forceinline__ void take_transposed(uint32_t (&w)[32]) const
+    {
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            uint32_t r[4];
+            load_blocks_transposed(addr + static_cast<uint32_t>(lane * 128 + ((c ^ (lane & 7)) << 4)), r);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[4 * c + e] = r[e];
+        }
+    }
+    __device__ __forceinline__ void transposed(const uint32_t (&w)[32]) const
     {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const uint32_t at = addr + static_cast<uint32_t>(j * 128 + lane * 2);
-            asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at), "h"(static_cast<uint16_t>(w[j] & 0xFFFFu)) : "memory");
-            asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at + 64u), "h"(static_cast<uint16_t>(w[j] >> 16))
-                         : "memory");
+        for (int c = 0; c < 8; ++c) {
+            const int j = c * 8 + lane % 8; // row: the block's column
+            const uint32_t r[4] = {w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]};
+            store_blocks(addr + static_cast<uint32_t>(j * 64 + (((lane / 8) ^ ((j >> 1) & 3)) << 4)), r);
         }
     }
     // 32 rows of 32 four-byte elements, this lane's column.
@@ -323,6 +352,11 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
         mbar_init(mma_done, 1);
         fence_barrier_init();
     }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_map(&maps.left);
+        tma_prefetch_map(&maps.right);
+        tma_prefetch_map(&maps.store);
+    }
     if (warp == 1) {
         tmem_alloc(tmem_slot, T::kTmemCols);
         tmem_relinquish();
@@ -364,17 +398,11 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
                         const uint32_t dst = base + static_cast<uint32_t>(f % S) * T::kStageBytes;
                         const uint32_t full = ring.full_bar(f);
                         ring.producer_commit(f, T::kStageBytes);
-#pragma unroll
-                        for (int q = 0; q < BM / kBox; ++q)
-                            tma_load_3d(dst + q * kBoxBytes, lmap, full, lx, row0 + q * kBox, lz);
-#pragma unroll
-                        for (int q = 0; q < BN / kBox; ++q) {
-                            const uint32_t to = dst + T::kLeftBytes + q * kBoxBytes;
-                            if constexpr (RightMN)
-                                tma_load_3d(to, rmap, full, col0 + q * kBox, k, rz);
-                            else
-                                tma_load_3d(to, rmap, full, rx, col0 + q * kBox, rz);
-                        }
+                        tma_load_3d(dst, lmap, full, lx, row0, lz);
+                        if constexpr (RightMN)
+                            tma_load_4d(dst + T::kLeftBytes, rmap, full, 0, k, col0 / 64, rz);
+                        else
+                            tma_load_3d(dst + T::kLeftBytes, rmap, full, rx, col0, rz);
                     }
                 }
             }
@@ -424,7 +452,7 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
                         // K step: 32 bytes along a K-major row; 16 rows of 128
                         // bytes of an MN-major box.
                         const uint64_t bdesc =
-                            RightMN ? smem_desc_sw128(b_addr + ks * kUmmaK * 128, kBoxBytes, 1024)
+                            RightMN ? smem_desc_sw128(b_addr + ks * kUmmaK * 128, kAtomBytes, 1024)
                                     : smem_desc_sw128(b_addr + ks * kUmmaK * 2, 16, 1024);
 #pragma unroll
                         for (int h = 0; h < MH; ++h) {
@@ -457,7 +485,8 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
         const int epi = warp - 2;
         const int half = MH == 2 ? epi / 4 : 0;                      // of the tile's rows
         const int first_col = MH == 2 ? 0 : (epi / 4) * T::kEpiCols; // of the tile's columns
-        const Staging staging{staging0 + static_cast<uint32_t>(epi) * kStagingBytes, lane};
+        Staging staging{staging0 + static_cast<uint32_t>(epi) * kStagingBytes, 0, lane};
+        static_assert(T::kEpiWarps * kLentBufs * kStagingBytes <= S * T::kStageBytes, "the ring has room to lend");
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         int acc = 0; // accumulators taken
         for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
@@ -472,17 +501,19 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
             const int row = row0 + lane;
             const bool mirrored = symmetric && at.i != at.j;
 
-            // 64 columns of a finished accumulator, added to v.
-            auto take = [&](int slot, int column, float (&v)[64]) {
+            // 64 columns of a finished accumulator, in pairs, to v or added to it.
+            auto take = [&](int slot, int column, bool add, unsigned long long (&v)[32]) {
                 uint32_t r0[32], r1[32];
                 const uint32_t taddr = tmem_base + lanes + static_cast<uint32_t>((slot * MH + half) * BN + column);
                 tmem_ld_32x32b_x32(taddr, r0);
                 tmem_ld_32x32b_x32(taddr + 32u, r1);
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    v[j] += __uint_as_float(r0[j]);
-                    v[32 + j] += __uint_as_float(r1[j]);
+                for (int j = 0; j < 16; ++j) {
+                    const unsigned long long a = pair(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]));
+                    const unsigned long long b = pair(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]));
+                    v[j] = add ? add2(v[j], a) : a;
+                    v[16 + j] = add ? add2(v[16 + j], b) : b;
                 }
             };
             // Wait for accumulator `acc`; false when the wait ran out.
@@ -505,18 +536,25 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
                     mbar_arrive(tmem_empty0 + 8u * (acc % T::kAccBufs));
                 ++acc;
             };
+            // Past the last accumulator of the CTA's last tile: every copy has
+            // landed and been multiplied.
+            auto borrow = [&]() {
+                if (t + static_cast<int>(gridDim.x) >= num_tiles)
+                    staging.lent = base + static_cast<uint32_t>(epi * kLentBufs) * kStagingBytes;
+            };
             // 64 columns of this warp's 32 rows, scaled and stored.
-            auto emit = [&](float (&v)[64], int col0) {
+            auto emit = [&](unsigned long long (&v)[32], int col0) {
+                const unsigned long long scale = pair(alpha, alpha);
 #pragma unroll
-                for (int j = 0; j < 64; ++j)
-                    v[j] *= alpha;
+                for (int j = 0; j < 32; ++j)
+                    v[j] = mul2(v[j], scale);
                 if (p.diag != 0.0f && row0 < col0 + 64 && col0 < row0 + 32) {
 #pragma unroll
-                    for (int j = 0; j < 64; ++j)
-                        if (col0 + j == row)
-                            v[j] += diag;
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = add2(v[j], pair(col0 + 2 * j == row ? diag : 0.0f, col0 + 2 * j + 1 == row ? diag : 0.0f));
                 }
                 uint32_t w[32];
+                float lo, hi;
                 if (p.output == kPlanes) {
                     const bool on_diag = p.diag_plane != 0 && row0 / kDiagBlock == col0 / kDiagBlock;
                     const int planes = p.planes + (on_diag ? 1 : 0);
@@ -525,10 +563,16 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
                         const bool extra = q == p.planes;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
-                            w[j] = pack_f16(v[2 * j], v[2 * j + 1]);
-                            const float2 kept = unpack_f16(w[j]);
-                            v[2 * j] -= kept.x; // exact: what this plane leaves over
-                            v[2 * j + 1] -= kept.y;
+                            split(v[j], lo, hi);
+                            w[j] = pack_f16(lo, hi);
+                        }
+                        if (q + 1 < planes) { // what this plane leaves over, exactly
+                            const unsigned long long minus = pair(-1.0f, -1.0f);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const float2 kept = unpack_f16(w[j]);
+                                v[j] = fma2(pair(kept.x, kept.y), minus, v[j]);
+                            }
                         }
                         staging.begin();
                         staging.row(w);
@@ -537,8 +581,9 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
                         else
                             staging.end(&maps.store, col0, row0, at.b * p.planes_pitch + q);
                         if (mirrored) {
+                            staging.take_transposed(w);
                             staging.begin();
-                            staging.column16(w);
+                            staging.transposed(w);
                             if (extra)
                                 staging.end(&maps.mirror_diag, row0 % kDiagBlock, col0, at.b);
                             else
@@ -547,14 +592,18 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
                     }
                 } else if (p.out_tma && p.output == kBf16) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+                    for (int j = 0; j < 32; ++j) {
+                        split(v[j], lo, hi);
+                        w[j] = pack_bf16(lo, hi);
+                    }
                     staging.begin();
+                    staging.row(w);
                     if (p.transposed) {
-                        staging.column16(w);
+                        staging.take_transposed(w);
+                        __syncwarp();
+                        staging.transposed(w);
                         staging.end(&maps.store, row0, col0, at.b);
                     } else {
-                        staging.row(w);
                         staging.end(&maps.store, col0, row0, at.b);
                     }
                 } else if (p.out_tma) {
@@ -563,8 +612,11 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
                         if (col0 + 32 * h >= p.cols)
                             break; // warp-uniform
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            w[j] = __float_as_uint(v[32 * h + j]);
+                        for (int j = 0; j < 16; ++j) {
+                            split(v[16 * h + j], lo, hi);
+                            w[2 * j] = __float_as_uint(lo);
+                            w[2 * j + 1] = __float_as_uint(hi);
+                        }
                         staging.begin();
                         if (p.transposed) {
                             staging.column32(w);
@@ -583,7 +635,8 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
                         if (col0 + j < p.cols) {
                             const long long o = first + (p.transposed ? (col0 + j) * p.ldo + row
                                                                       : row * p.ldo + col0 + j);
-                            store_f32(p.out, p.output == kBf16, o, v[j]);
+                            split(v[j / 2], lo, hi);
+                            store_f32(p.out, p.output == kBf16, o, j & 1 ? hi : lo);
                         }
                     }
                 }
@@ -591,36 +644,35 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
 
             if constexpr (T::kEpiCols == 64) {
                 const int parts = tile_blocks<BM, BN>(p, at).accumulators(p.fine != 0);
-                float v[64];
+                unsigned long long v[32];
 #pragma unroll
-                for (int j = 0; j < 64; ++j)
-                    v[j] = 0.0f;
+                for (int j = 0; j < 32; ++j)
+                    v[j] = 0ull;
                 bool ok = true;
                 for (int part = 0; part < parts && ok; ++part) {
                     ok = wait_full();
                     if (ok) {
-                        take(acc % T::kAccBufs, first_col, v);
+                        take(acc % T::kAccBufs, first_col, true, v);
                         release();
                     }
                 }
                 if (!ok)
                     break;
+                borrow();
                 const int col0 = at.j * BN + first_col;
                 if (row0 < p.rows && col0 < p.cols) // warp-uniform
                     emit(v, col0);
             } else {
                 if (!wait_full())
                     break;
+                borrow();
 #pragma unroll 1
                 for (int c = 0; c < T::kEpiCols; c += 64) {
                     const int col0 = at.j * BN + first_col + c;
                     if (col0 >= p.cols || row0 >= p.rows)
                         break; // warp-uniform: nothing of this box lies in the matrix
-                    float v[64];
-#pragma unroll
-                    for (int j = 0; j < 64; ++j)
-                        v[j] = 0.0f;
-                    take(acc % T::kAccBufs, first_col + c, v);
+                    unsigned long long v[32];
+                    take(acc % T::kAccBufs, first_col + c, false, v);
                     emit(v, col0);
                 }
                 release();
@@ -858,10 +910,27 @@ struct Planes {
     int rows, cols, pitch, planes; // planes: over the whole batch
 };
 
-int encode(CUtensorMap *map, const Planes &m, int box_cols, int box_rows, bool swizzle)
+int encode(CUtensorMap *map, const Planes &m, uint32_t box_cols, uint32_t box_rows, int swizzle)
 {
-    return encode_tensor_map_3d(map, kElement16, m.base, m.cols, m.rows, m.planes, static_cast<uint64_t>(m.pitch) * 2u,
-                                static_cast<uint64_t>(m.pitch) * 2u * m.rows, box_cols, box_rows, swizzle);
+    const uint64_t pitch = static_cast<uint64_t>(m.pitch) * 2u;
+    const uint64_t dims[3] = {static_cast<uint64_t>(m.cols), static_cast<uint64_t>(m.rows),
+                              static_cast<uint64_t>(m.planes)};
+    const uint64_t pitches[2] = {pitch, pitch * static_cast<uint64_t>(m.rows)};
+    const uint32_t box[3] = {box_cols, box_rows, 1};
+    return encode_tensor_map(map, kElement16, m.base, 3, dims, pitches, box, swizzle);
+}
+
+// The columns in groups of 64, `columns` of them and 64 rows a box.  The last
+// group may reach past the matrix into its rows' padding; what is computed
+// from that lies outside the result.
+int encode_column_groups(CUtensorMap *map, const Planes &m, uint32_t columns)
+{
+    const uint64_t pitch = static_cast<uint64_t>(m.pitch) * 2u;
+    const uint64_t dims[4] = {64, static_cast<uint64_t>(m.rows), static_cast<uint64_t>(m.pitch / 64),
+                              static_cast<uint64_t>(m.planes)};
+    const uint64_t pitches[3] = {pitch, 128, pitch * static_cast<uint64_t>(m.rows)};
+    const uint32_t box[4] = {64, BK, columns / 64, 1};
+    return encode_tensor_map(map, kElement16, m.base, 4, dims, pitches, box, 128);
 }
 
 template <class Kernel, class... Args>
@@ -899,22 +968,23 @@ int launch_product_t(const Maps &maps, const Product &p, const Device &d, cudaSt
 }
 
 // 256 x 256 tiles feed each right-hand slice to two MMAs, 128 x 128 ones
-// leave fewer SMs idle when there are few.
-bool use_large_tile(const Product &p, int sms)
+// leave fewer SMs idle when there are few (and are the ones that can sum
+// several accumulators).
+bool use_large_tile(bool symmetric, int rows, int cols, int batch, bool fine, int sms)
 {
     auto rounds = [&](int side) {
-        const long long tiles = static_cast<long long>(tiles_of(p.symmetric != 0, (p.rows + side - 1) / side,
-                                                                (p.cols + side - 1) / side)) * p.batch;
+        const long long tiles =
+            static_cast<long long>(tiles_of(symmetric, (rows + side - 1) / side, (cols + side - 1) / side)) * batch;
         return (tiles + sms - 1) / sms;
     };
-    return !p.fine && rounds(256) * 4 * 2 <= rounds(128) * 3;
+    return !fine && rounds(256) * 4 * 2 <= rounds(128) * 3;
 }
 
 template <bool RightMN>
-int launch_product(const Maps &maps, const Product &p, const Device &d, cudaStream_t s)
+int launch_product(bool large, const Maps &maps, const Product &p, const Device &d, cudaStream_t s)
 {
-    return use_large_tile(p, d.sms) ? launch_product_t<2, 256, 3, RightMN>(maps, p, d, s)
-                                    : launch_product_t<1, 128, 4, RightMN>(maps, p, d, s);
+    return large ? launch_product_t<2, 256, 3, RightMN>(maps, p, d, s)
+                 : launch_product_t<1, 128, 4, RightMN>(maps, p, d, s);
 }
 
 struct Call {
@@ -941,51 +1011,57 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
     const Planes q_diag{ws + l.q_diag, l.r, kDiagBlock, kDiagBlock, nb};
     float *f = reinterpret_cast<float *>(ws + l.f);
 
-    Maps from_x[2], from_a, from_qx[2]; // X X^T -> A (or Q); A A -> Q; Q X -> X
-    alignas(64) CUtensorMap to_out;
+    // The tiles of X X^T and of the square, and of Q X.
+    const bool large_a = use_large_tile(true, l.r, l.r, nb, wide_result, d.sms);
+    const bool large_x = use_large_tile(false, l.r, l.c, nb, wide_result, d.sms);
+    const uint32_t side_a = large_a ? 256 : 128, side_x = large_x ? 256 : 128;
+    CUtensorMap x_load[2], x_columns[2], a_load, a_diag_load, q_load, q_diag_load;
+    CUtensorMap to_x[2], to_a[4], to_q[4], to_out; // a and q: store, mirror, store_diag, mirror_diag
     int st = GEMM_OK;
-    auto enc = [&](CUtensorMap *map, const Planes &m, int cols, int rows, bool swizzle) {
+    auto enc = [&](CUtensorMap *map, const Planes &m, uint32_t cols, uint32_t rows, int swizzle) {
         if (st == GEMM_OK)
             st = encode(map, m, cols, rows, swizzle);
     };
-    std::memset(&from_a, 0, sizeof from_a);
-    enc(&from_a.left, a, kBox, kBox, true);
-    enc(&from_a.left_diag, a_diag, kBox, kBox, true);
-    from_a.right = from_a.left;
-    from_a.right_diag = from_a.left_diag;
-    enc(&from_a.store, q, 64, 32, true);
-    enc(&from_a.mirror, q, 32, 64, false);
-    enc(&from_a.store_diag, q_diag, 64, 32, true);
-    enc(&from_a.mirror_diag, q_diag, 32, 64, false);
-    Maps to_a = from_a; // the stores into A
-    enc(&to_a.store, a, 64, 32, true);
-    enc(&to_a.mirror, a, 32, 64, false);
-    enc(&to_a.store_diag, a_diag, 64, 32, true);
-    enc(&to_a.mirror_diag, a_diag, 32, 64, false);
-    CUtensorMap q_load, q_diag_load;
-    enc(&q_load, q, kBox, kBox, true);
-    enc(&q_diag_load, q_diag, kBox, kBox, true);
     for (int i = 0; i < 2; ++i) {
-        from_x[i] = to_a;
-        enc(&from_x[i].left, x[i], kBox, kBox, true);
-        from_x[i].right = from_x[i].left;
-        from_qx[i] = from_a;
-        from_qx[i].left = q_load;
-        from_qx[i].left_diag = q_diag_load;
-        from_qx[i].right = from_x[i].right;
-        enc(&from_qx[i].store, x[1 - i], 64, 32, true);
+        enc(&x_load[i], x[i], BK, side_a, 128);
+        if (st == GEMM_OK)
+            st = encode_column_groups(&x_columns[i], x[i], side_x);
+        enc(&to_x[i], x[i], 64, 32, 128);
     }
+    enc(&a_load, a, BK, side_a, 128);
+    enc(&a_diag_load, a_diag, BK, side_a, 128);
+    enc(&q_load, q, BK, side_x, 128);
+    enc(&q_diag_load, q_diag, BK, side_x, 128);
+    auto stores = [&](CUtensorMap *to, const Planes &m, const Planes &m_diag) {
+        enc(&to[0], m, 64, 32, 128);
+        enc(&to[1], m, 32, 64, 64);
+        enc(&to[2], m_diag, 64, 32, 128);
+        enc(&to[3], m_diag, 32, 64, 64);
+    };
+    stores(to_a, a, a_diag);
+    stores(to_q, q, q_diag);
     if (st != GEMM_OK)
         return st;
+    auto set_stores = [](Maps &maps, const CUtensorMap *to) {
+        maps.store = to[0];
+        maps.mirror = to[1];
+        maps.store_diag = to[2];
+        maps.mirror_diag = to[3];
+    };
+    Maps maps;
+    std::memset(&maps, 0, sizeof maps);
     const uint64_t es = wide_result ? 4 : 2;
     const bool out_tma = (reinterpret_cast<uintptr_t>(call.out) & 15u) == 0 && (call.ldo * es) % 16 == 0 &&
                          (nb == 1 || (call.o_batch * es) % 16 == 0);
     std::memset(&to_out, 0, sizeof to_out);
     if (out_tma) {
-        const uint64_t plane_pitch = nb == 1 ? call.ldo * es * static_cast<uint64_t>(call.m) : call.o_batch * es;
-        const uint32_t box_cols = wide_result || tall ? 32 : 64, box_rows = tall && !wide_result ? 64 : 32;
-        st = encode_tensor_map_3d(&to_out, wide_result ? kElement32 : kElement16, call.out, call.n, call.m, nb,
-                                  call.ldo * es, plane_pitch, box_cols, box_rows, !tall);
+        const uint64_t dims[3] = {static_cast<uint64_t>(call.n), static_cast<uint64_t>(call.m),
+                                  static_cast<uint64_t>(nb)};
+        const uint64_t pitches[2] = {call.ldo * es,
+                                     nb == 1 ? call.ldo * es * static_cast<uint64_t>(call.m) : call.o_batch * es};
+        const uint32_t box[3] = {wide_result || tall ? 32u : 64u, tall && !wide_result ? 64u : 32u, 1};
+        st = encode_tensor_map(&to_out, wide_result ? kElement32 : kElement16, call.out, 3, dims, pitches, box,
+                               !tall ? 128 : wide_result ? 0 : 64);
         if (st != GEMM_OK)
             return st;
     }
@@ -1049,14 +1125,9 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
             p.alpha_power = first ? 3 : 0;
             p.diag_power = first ? 1 : 0;
         }
-        Maps maps = from_x[cur];
-        if (cc == 0.0f) {
-            maps.store = from_a.store;
-            maps.mirror = from_a.mirror;
-            maps.store_diag = from_a.store_diag;
-            maps.mirror_diag = from_a.mirror_diag;
-        }
-        st = launch_product<false>(maps, p, d, s);
+        maps.left = maps.right = x_load[cur];
+        set_stores(maps, cc != 0.0f ? to_a : to_q);
+        st = launch_product<false>(large_a, maps, p, d, s);
         if (st != GEMM_OK)
             return st;
 
@@ -1079,7 +1150,10 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
             p.alpha = kScaleQ * cc / (kScaleA * kScaleA);
             p.diag = kScaleQ * static_cast<float>(ca - static_cast<double>(cb) * cb / (4.0 * cc));
             p.alpha_power = p.diag_power = first ? 1 : 0;
-            st = launch_product<false>(from_a, p, d, s);
+            maps.left = maps.right = a_load;
+            maps.left_diag = maps.right_diag = a_diag_load;
+            set_stores(maps, to_q);
+            st = launch_product<false>(large_a, maps, p, d, s);
             if (st != GEMM_OK)
                 return st;
         }
@@ -1104,7 +1178,10 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
             add(p, 0, 1, kAll);
         }
         add(p, 0, 0, kAll);
-        maps = from_qx[cur];
+        maps.left = q_load;
+        maps.left_diag = q_diag_load;
+        maps.right = x_columns[cur];
+        maps.store = last ? to_out : to_x[1 - cur];
         if (last) {
             p.output = wide_result ? kF32 : kBf16;
             p.alpha = 1.0f / (kScaleQ * kScaleX);
@@ -1113,7 +1190,6 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
             p.out = call.out;
             p.ldo = call.ldo;
             p.out_batch = call.o_batch;
-            maps.store = to_out;
         } else {
             p.output = kPlanes;
             // The last step reads one plane less.
@@ -1121,7 +1197,7 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
             p.planes_pitch = l.xp;
             p.alpha = 1.0f / kScaleQ;
         }
-        st = launch_product<true>(maps, p, d, s);
+        st = launch_product<true>(large_x, maps, p, d, s);
         if (st != GEMM_OK)
             return st;
     }

@@ -52,35 +52,6 @@ struct Shape {
     int withhold;
 };
 
-// ------------------------------------------------------------ pairs
-__device__ __forceinline__ unsigned long long pair(float a, float b)
-{
-    unsigned long long v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
-    return v;
-}
-__device__ __forceinline__ void split(unsigned long long v, float &a, float &b)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b)
-{
-    unsigned long long r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b)
-{
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c)
-{
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 // a / n for a positive n whose reciprocal is `inv`: the product, corrected by
 // what it is off (exact where the quotient is, as a constant row's mean).
 __device__ __forceinline__ float divided(float a, float n, float inv)
@@ -88,13 +59,6 @@ __device__ __forceinline__ float divided(float a, float n, float inv)
     const float q = a * inv;
     return isfinite(q) ? fmaf(fmaf(-q, n, a), inv, q) : q;
 }
-__device__ __forceinline__ float both(unsigned long long v)
-{
-    float a, b;
-    split(v, a, b);
-    return a + b;
-}
-
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll

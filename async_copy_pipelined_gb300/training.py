@@ -52,6 +52,13 @@ def _load():
     return _torch
 
 
+def _raw_stream(index):
+    """The current stream's handle (torch's own short cut to it where it has
+    one: building a Stream object takes longer than the launch)."""
+    short = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+    return short(index) if short is not None else _torch.cuda.current_stream(index).cuda_stream
+
+
 def _dtype(t, name):
     code = _CODES.get(t.dtype)
     if code is None:
@@ -119,9 +126,9 @@ def _enter(device, stream):
     torch = _torch
     if device.type != "cuda":
         raise ValueError("operands must be CUDA tensors")
-    cur = torch.cuda.current_stream(device)
     if stream is None:
-        return cur.cuda_stream, None
+        return _raw_stream(device.index), None
+    cur = torch.cuda.current_stream(device)
     if getattr(stream, "device", device) != device:
         raise ValueError(f"stream belongs to {stream.device}, operands to {device}")
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
