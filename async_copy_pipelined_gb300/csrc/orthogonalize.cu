@@ -107,6 +107,7 @@ struct Product {
     int left_planes, right_planes;
     int passes;
     Pass pass[kMaxPasses];
+    int ranks; // CTAs that share a tile's K blocks
     int fine; // an accumulator for each K block of the last pass, one for the passes before it
     float alpha, diag;
     int alpha_power, diag_power; // of f
@@ -129,7 +130,13 @@ struct Product {
 // warps take a quarter's 256 columns in turn; the 128 x 128 tile has four
 // accumulators and each warp takes 64 columns at once, so that it can also
 // sum a tile's accumulators in registers (Product.fine).
-template <int MH, int BN, int S>
+//
+// Split: where the 128 x 128 tiles are fewer than half the SMs, a cluster of
+// 2, 4 or 8 CTAs shares a tile's K blocks, each multiplying its run of them.
+// A tile is eight units of 32 rows by 64 columns, one per epilogue warp; each
+// rank owns 8 / ranks of them, receives the other ranks' sums of those into
+// its shared memory, adds them in rank order and stores them.
+template <int MH, int BN, int S, bool Split>
 struct Tile {
     static constexpr int BM = kUmmaM * MH;
     static constexpr uint32_t kLeftBytes = BM * BK * 2;
@@ -139,8 +146,12 @@ struct Tile {
     static constexpr int kEpiWarps = 8;
     static constexpr int kEpiCols = MH * BN / 2; // columns per epilogue warp
     static constexpr int kThreads = (2 + kEpiWarps) * 32;
-    static constexpr int kSmem = S * kStageBytes + kEpiWarps * kStagingBytes + 1024 /* barriers */ + 1024 /* slack */;
+    static constexpr uint32_t kUnitBytes = 32 * 64 * 4;
+    static constexpr uint32_t kReceiveBytes = Split ? kEpiWarps * kUnitBytes : 0;
+    static constexpr int kSmem = S * kStageBytes + kEpiWarps * kStagingBytes + kReceiveBytes + 1024 /* barriers */ +
+                                 1024 /* slack */;
     static_assert(MH * BN <= 512 && kEpiCols % 64 == 0, "accumulators fit tensor memory");
+    static_assert(!Split || kEpiCols == 64, "a unit is what one warp holds");
 };
 
 // Tile t of the batch: matrix b, tile row i, tile column j.  The upper
@@ -192,24 +203,27 @@ __device__ __forceinline__ void pass_range(const Pass &pass, int k, int row0, in
 // K blocks of one tile: of all its passes but the last, and of all.
 struct Blocks {
     int before, all;
+    int lo, hi; // this CTA's
     // Whether an accumulator ends with block kb, and how many there are.
-    __device__ __forceinline__ bool ends(int kb, bool fine) const { return kb == all - 1 || (fine && kb >= before - 1); }
+    __device__ __forceinline__ bool ends(int kb, bool fine) const { return kb == hi - 1 || (fine && kb >= before - 1); }
     __device__ __forceinline__ int accumulators(bool fine) const
     {
-        return fine ? (before > 0 ? 1 : 0) + all - before : 1;
+        return fine ? (lo < min(before, hi) ? 1 : 0) + max(0, hi - max(lo, before)) : (lo < hi ? 1 : 0);
     }
 };
 
 template <int BM, int BN>
-__device__ __forceinline__ Blocks tile_blocks(const Product &p, const TileAt &at)
+__device__ __forceinline__ Blocks tile_blocks(const Product &p, const TileAt &at, int rank)
 {
-    Blocks n{0, 0};
+    Blocks n{0, 0, 0, 0};
     for (int ps = 0; ps < p.passes; ++ps) {
         int k0, blocks;
         pass_range<BM, BN>(p.pass[ps], p.k, at.i * BM, at.j * BN, k0, blocks);
         n.before = n.all;
         n.all += blocks;
     }
+    n.lo = rank * n.all / p.ranks;
+    n.hi = (rank + 1) * n.all / p.ranks;
     return n;
 }
 
@@ -311,11 +325,11 @@ struct Staging {
 
 // RightMN: the right operand's rows are k (Q X); otherwise its rows are D's
 // columns (X X^T, and the symmetric A A).
-template <int MH, int BN, int S, bool RightMN>
-__global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
+template <int MH, int BN, int S, bool RightMN, bool Split>
+__global__ void __launch_bounds__(Tile<MH, BN, S, Split>::kThreads, 1)
     product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Product p)
 {
-    using T = Tile<MH, BN, S>;
+    using T = Tile<MH, BN, S, Split>;
     constexpr int BM = T::BM;
     // Instruction descriptor, kind::f16: D float32 (bits 4-5 = 1), A and B
     // float16 (bits 7-12 = 0), A K-major, B K-major or MN-major (bit 16),
@@ -326,7 +340,8 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = align_smem(raw, 1024);
     const uint32_t staging0 = base + S * T::kStageBytes;
-    const uint32_t bars = staging0 + T::kEpiWarps * kStagingBytes;
+    const uint32_t receive0 = staging0 + T::kEpiWarps * kStagingBytes;
+    const uint32_t bars = receive0 + T::kReceiveBytes;
     const TmaRing<S> ring{bars, bars + 8u * S};
     const uint32_t tmem_full0 = bars + 16u * S;                  // [kAccBufs]
     const uint32_t tmem_empty0 = tmem_full0 + 8u * T::kAccBufs; // [kAccBufs]
@@ -341,6 +356,10 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
     const int tiles_m = (p.rows + BM - 1) / BM;
     const int tiles_n = (p.cols + BN - 1) / BN;
     const int num_tiles = tiles_of(symmetric, tiles_m, tiles_n) * p.batch;
+    // A split tile has a cluster of its own, so each CTA has one tile.
+    const int rank = Split ? static_cast<int>(cluster_cta_rank()) : 0;
+    const int first_tile = Split ? static_cast<int>(blockIdx.x) / p.ranks : static_cast<int>(blockIdx.x);
+    const int tile_step = Split ? num_tiles : static_cast<int>(gridDim.x);
 
     if (threadIdx.x == 0) {
         ring.init(1);
@@ -362,7 +381,10 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
         tmem_relinquish();
     }
     tc_fence_before_sync();
-    __syncthreads();
+    if constexpr (Split)
+        cluster_sync(); // every CTA of the cluster has started
+    else
+        __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot_ptr;
     grid_launch_next();
@@ -373,19 +395,23 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
         if (lane == 0) {
             int f = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+            for (int t = first_tile; t < num_tiles && ok; t += tile_step) {
                 const TileAt at = tile_at(t, symmetric, tiles_m, tiles_n);
                 const int row0 = at.i * BM, col0 = at.j * BN;
+                const Blocks all = tile_blocks<BM, BN>(p, at, rank);
+                int before = 0; // K blocks of the passes before this one
                 for (int ps = 0; ps < p.passes && ok; ++ps) {
                     const Pass pass = p.pass[ps];
                     int k0, blocks;
                     pass_range<BM, BN>(pass, p.k, row0, col0, k0, blocks);
+                    const int kb_lo = max(0, all.lo - before), kb_hi = min(blocks, all.hi - before);
+                    before += blocks;
                     const bool ld = pass.left < 0, rd = pass.right < 0;
                     const CUtensorMap *lmap = ld ? &maps.left_diag : &maps.left;
                     const CUtensorMap *rmap = rd ? &maps.right_diag : &maps.right;
                     const int lz = ld ? at.b : at.b * p.left_planes + pass.left;
                     const int rz = rd ? at.b : at.b * p.right_planes + pass.right;
-                    for (int kb = 0; kb < blocks; ++kb, ++f) {
+                    for (int kb = kb_lo; kb < kb_hi; ++kb, ++f) {
                         if (f == p.withhold)
                             continue; // test hook: this position is never filled
                         if (!ring.producer_acquire(f, p.wait_limit_ns)) {
@@ -414,18 +440,20 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
             if (!drained)
                 record_error(p.status, kErrFamilyOrthogonalize | kErrRoleDrain);
         }
+        if constexpr (Split)
+            cluster_sync(); // the epilogue's exchange
     } else if (warp == 1) {
         // ------------------------------------------------------- MMA issuer
         if (lane == 0) {
             int f = 0;
             bool ok = true;
             int acc = 0; // accumulators begun
-            for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+            for (int t = first_tile; t < num_tiles && ok; t += tile_step) {
                 const TileAt at = tile_at(t, symmetric, tiles_m, tiles_n);
-                const Blocks blocks = tile_blocks<BM, BN>(p, at);
+                const Blocks blocks = tile_blocks<BM, BN>(p, at, rank);
                 uint32_t d_tmem = tmem_base, full_bar = tmem_full0;
                 bool fresh = true; // the next block begins an accumulator
-                for (int kb = 0; kb < blocks.all; ++kb, ++f) {
+                for (int kb = blocks.lo; kb < blocks.hi; ++kb, ++f) {
                     if (fresh) {
                         const int slot = acc % T::kAccBufs;
                         const uint32_t use_parity = static_cast<uint32_t>((acc / T::kAccBufs) & 1);
@@ -473,6 +501,8 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
             if (!mbar_wait_bounded(mma_done, 0, p.wait_limit_ns))
                 record_error(p.status, kErrFamilyOrthogonalize | kErrRoleDrain);
         }
+        if constexpr (Split)
+            cluster_sync(); // the epilogue's exchange
         __syncwarp();
         if (!mbar_wait_bounded(epi_done, 0, p.wait_limit_ns) && lane == 0)
             record_error(p.status, kErrFamilyOrthogonalize | kErrRoleDrain);
@@ -489,7 +519,7 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
         static_assert(T::kEpiWarps * kLentBufs * kStagingBytes <= S * T::kStageBytes, "the ring has room to lend");
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         int acc = 0; // accumulators taken
-        for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
+        for (int t = first_tile; t < num_tiles; t += tile_step) {
             const TileAt at = tile_at(t, symmetric, tiles_m, tiles_n);
             const float f = p.f[at.b];
             float alpha = p.alpha, diag = p.diag;
@@ -539,7 +569,7 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
             // Past the last accumulator of the CTA's last tile: every copy has
             // landed and been multiplied.
             auto borrow = [&]() {
-                if (t + static_cast<int>(gridDim.x) >= num_tiles)
+                if (t + tile_step >= num_tiles)
                     staging.lent = base + static_cast<uint32_t>(epi * kLentBufs) * kStagingBytes;
             };
             // 64 columns of this warp's 32 rows, scaled and stored.
@@ -643,7 +673,7 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
             };
 
             if constexpr (T::kEpiCols == 64) {
-                const int parts = tile_blocks<BM, BN>(p, at).accumulators(p.fine != 0);
+                const int parts = tile_blocks<BM, BN>(p, at, rank).accumulators(p.fine != 0);
                 unsigned long long v[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
@@ -656,11 +686,45 @@ __global__ void __launch_bounds__(Tile<MH, BN, S>::kThreads, 1)
                         release();
                     }
                 }
+                bool mine = ok;
+                if constexpr (Split) {
+                    // This warp's unit goes to its owner, or gathers the other
+                    // ranks' sums of it: 16 bytes of 32 lanes side by side.
+                    const int unit = quarter * 2 + epi / 4, each = T::kEpiWarps / p.ranks;
+                    const int owner = unit / each;
+                    const uint32_t slots = receive0 + static_cast<uint32_t>(unit % each * p.ranks) * T::kUnitBytes;
+                    mine = ok && owner == rank;
+                    if (ok && owner != rank) {
+                        const uint32_t to = map_to_cta(slots + static_cast<uint32_t>(rank) * T::kUnitBytes,
+                                                       static_cast<uint32_t>(owner)) +
+                                            static_cast<uint32_t>(lane) * 16u;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            float a, b, c, d;
+                            split(v[j], a, b);
+                            split(v[j + 1], c, d);
+                            st_cluster_v4(to + static_cast<uint32_t>(j) * 256u, __float_as_uint(a), __float_as_uint(b),
+                                          __float_as_uint(c), __float_as_uint(d));
+                        }
+                    }
+                    cluster_sync(); // also in a CTA whose wait ran out
+                    for (int src = 0; src < p.ranks && mine; ++src) {
+                        if (src == rank)
+                            continue;
+                        const uint8_t *from = smem_raw + (slots - raw) + src * T::kUnitBytes + lane * 16;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const float4 q = *reinterpret_cast<const float4 *>(from + j * 256);
+                            v[j] = add2(v[j], pair(q.x, q.y));
+                            v[j + 1] = add2(v[j + 1], pair(q.z, q.w));
+                        }
+                    }
+                }
                 if (!ok)
                     break;
                 borrow();
                 const int col0 = at.j * BN + first_col;
-                if (row0 < p.rows && col0 < p.cols) // warp-uniform
+                if (mine && row0 < p.rows && col0 < p.cols) // warp-uniform
                     emit(v, col0);
             } else {
                 if (!wait_full())
@@ -933,19 +997,31 @@ int encode_column_groups(CUtensorMap *map, const Planes &m, uint32_t columns)
     return encode_tensor_map(map, kElement16, m.base, 4, dims, pitches, box, 128);
 }
 
+// `overlap`: the kernel may start while the one before it ends (it calls
+// grid_wait()); `cluster`: CTAs per cluster.
 template <class Kernel, class... Args>
-int launch(Kernel kernel, dim3 grid, int threads, int smem, bool overlap, cudaStream_t s, const Args &...args)
+int launch(Kernel kernel, dim3 grid, int threads, int smem, bool overlap, int cluster, cudaStream_t s,
+           const Args &...args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = overlap ? 1 : 0;
+    cudaLaunchAttribute attr[2] = {};
+    unsigned n = 0;
+    if (overlap) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
@@ -954,37 +1030,67 @@ struct Device {
     unsigned long long ctx;
 };
 
-template <int MH, int BN, int S, bool RightMN>
+template <int MH, int BN, int S, bool RightMN, bool Split>
 int launch_product_t(const Maps &maps, const Product &p, const Device &d, cudaStream_t s)
 {
-    using T = Tile<MH, BN, S>;
+    using T = Tile<MH, BN, S, Split>;
     static std::atomic<unsigned long long> limit_set[kMaxDevices];
-    if (ensure_smem_limit(product_kernel<MH, BN, S, RightMN>, T::kSmem, d.index, d.ctx, limit_set) != GEMM_OK)
+    auto *kernel = product_kernel<MH, BN, S, RightMN, Split>;
+    if (ensure_smem_limit(kernel, T::kSmem, d.index, d.ctx, limit_set) != GEMM_OK)
         return GEMM_ERR_CUDA;
     const long long tiles = static_cast<long long>(tiles_of(p.symmetric != 0, (p.rows + T::BM - 1) / T::BM,
                                                             (p.cols + BN - 1) / BN)) * p.batch;
-    const unsigned grid = static_cast<unsigned>(std::min<long long>(tiles, d.sms));
-    return launch(product_kernel<MH, BN, S, RightMN>, dim3(grid), T::kThreads, T::kSmem, true, s, maps, p);
+    const unsigned grid = static_cast<unsigned>(Split ? tiles * p.ranks : std::min<long long>(tiles, d.sms));
+    return launch(kernel, dim3(grid), T::kThreads, T::kSmem, true, p.ranks, s, maps, p);
 }
 
-// 256 x 256 tiles feed each right-hand slice to two MMAs, 128 x 128 ones
-// leave fewer SMs idle when there are few (and are the ones that can sum
-// several accumulators).
-bool use_large_tile(bool symmetric, int rows, int cols, int batch, bool fine, int sms)
+// How a product is cut: tiles of 256 x 256 or 128 x 128, the latter shared by
+// `ranks` CTAs.
+struct Cut {
+    bool large;
+    int ranks;
+};
+
+// By the time of one round of tiles, in microseconds measured on GB300: a K
+// block takes the 256 x 256 tile 0.65 and the 128 x 128 tile 0.34 (64 and 32
+// KiB at the 64 bytes a clock that an SM takes in), a K block with an
+// accumulator of its own 0.45; storing a tile takes about 4.5 and 1.5, an
+// exchange between ranks 1.  Ranks only where all tiles run at once.
+Cut choose_cut(bool symmetric, int rows, int cols, int batch, int k_blocks, bool fine, int sms)
 {
-    auto rounds = [&](int side) {
-        const long long tiles =
-            static_cast<long long>(tiles_of(symmetric, (rows + side - 1) / side, (cols + side - 1) / side)) * batch;
-        return (tiles + sms - 1) / sms;
+    auto tiles = [&](int side) {
+        return static_cast<long long>(tiles_of(symmetric, (rows + side - 1) / side, (cols + side - 1) / side)) * batch;
     };
-    return !fine && rounds(256) * 4 * 2 <= rounds(128) * 3;
+    const long long small = tiles(128);
+    const double block = fine ? 0.45 : 0.34;
+    Cut best{false, 1};
+    double least = static_cast<double>((small + sms - 1) / sms) * k_blocks * block + 1.5;
+    for (int ranks = 2; ranks <= 8; ranks *= 2) {
+        // Clusters of eight leave SMs of a GPC over: 128 of 152 CTAs run.
+        if (small * ranks > sms * 5 / 6 || k_blocks < 2 * ranks)
+            break;
+        const double t = (k_blocks + ranks - 1) / ranks * block + 2.5;
+        if (t < least) {
+            least = t;
+            best = Cut{false, ranks};
+        }
+    }
+    if (!fine) {
+        const long long rounds = (tiles(256) + sms - 1) / sms;
+        if (static_cast<double>(rounds) * (k_blocks * 0.65 + 4.5) < least)
+            best = Cut{true, 1};
+    }
+    return best;
 }
 
 template <bool RightMN>
-int launch_product(bool large, const Maps &maps, const Product &p, const Device &d, cudaStream_t s)
+int launch_product(const Cut &cut, const Maps &maps, Product p, const Device &d, cudaStream_t s)
 {
-    return large ? launch_product_t<2, 256, 3, RightMN>(maps, p, d, s)
-                 : launch_product_t<1, 128, 4, RightMN>(maps, p, d, s);
+    p.ranks = cut.ranks;
+    if (cut.large)
+        return launch_product_t<2, 256, 3, RightMN, false>(maps, p, d, s);
+    return cut.ranks > 1 ? launch_product_t<1, 128, 4, RightMN, true>(maps, p, d, s)
+                         : launch_product_t<1, 128, 4, RightMN, false>(maps, p, d, s);
 }
 
 struct Call {
@@ -1011,10 +1117,14 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
     const Planes q_diag{ws + l.q_diag, l.r, kDiagBlock, kDiagBlock, nb};
     float *f = reinterpret_cast<float *>(ws + l.f);
 
-    // The tiles of X X^T and of the square, and of Q X.
-    const bool large_a = use_large_tile(true, l.r, l.r, nb, wide_result, d.sms);
-    const bool large_x = use_large_tile(false, l.r, l.c, nb, wide_result, d.sms);
-    const uint32_t side_a = large_a ? 256 : 128, side_x = large_x ? 256 : 128;
+    // The cuts of X X^T, of the square and of Q X, for the K blocks of the
+    // passes a middle step makes.
+    const int kr = (l.r + BK - 1) / BK, kc = (l.c + BK - 1) / BK;
+    const Cut cut_a = choose_cut(true, l.r, l.r, nb, (wide_result ? 3 : 1) * kc, wide_result, d.sms);
+    const Cut cut_s = choose_cut(true, l.r, l.r, nb, (wide_result ? 3 : 1) * kr + std::min(kr, 4), wide_result, d.sms);
+    const Cut cut_x = choose_cut(false, l.r, l.c, nb, (wide_result ? 5 : 2) * kr + std::min(kr, 2), wide_result, d.sms);
+    const uint32_t side_a = cut_a.large ? 256 : 128, side_s = cut_s.large ? 256 : 128,
+                   side_x = cut_x.large ? 256 : 128;
     CUtensorMap x_load[2], x_columns[2], a_load, a_diag_load, q_load, q_diag_load;
     CUtensorMap to_x[2], to_a[4], to_q[4], to_out; // a and q: store, mirror, store_diag, mirror_diag
     int st = GEMM_OK;
@@ -1028,8 +1138,8 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
             st = encode_column_groups(&x_columns[i], x[i], side_x);
         enc(&to_x[i], x[i], 64, 32, 128);
     }
-    enc(&a_load, a, BK, side_a, 128);
-    enc(&a_diag_load, a_diag, BK, side_a, 128);
+    enc(&a_load, a, BK, side_s, 128);
+    enc(&a_diag_load, a_diag, BK, side_s, 128);
     enc(&q_load, q, BK, side_x, 128);
     enc(&q_diag_load, q_diag, BK, side_x, 128);
     auto stores = [&](CUtensorMap *to, const Planes &m, const Planes &m_diag) {
@@ -1074,12 +1184,12 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
     const uint64_t gs = call.dtype == GEMM_DTYPE_F32 ? 4 : 2;
     in.vec = (reinterpret_cast<uintptr_t>(call.G) & 15u) == 0 && (call.ldg * gs) % 16 == 0 &&
              (nb == 1 || (call.g_batch * gs) % 16 == 0);
-    st = launch(norm_kernel, dim3(l.parts, nb), kNormThreads, 0, false, s, in);
+    st = launch(norm_kernel, dim3(l.parts, nb), kNormThreads, 0, false, 1, s, in);
     if (st != GEMM_OK)
         return st;
     const dim3 pieces((l.c + 63) / 64, (l.r + 63) / 64, nb);
-    st = tall ? launch(planes_kernel<true>, pieces, kNormThreads, 0, true, s, in)
-              : launch(planes_kernel<false>, pieces, kNormThreads, 0, true, s, in);
+    st = tall ? launch(planes_kernel<true>, pieces, kNormThreads, 0, true, 1, s, in)
+              : launch(planes_kernel<false>, pieces, kNormThreads, 0, true, 1, s, in);
     if (st != GEMM_OK)
         return st;
 
@@ -1127,7 +1237,7 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
         }
         maps.left = maps.right = x_load[cur];
         set_stores(maps, cc != 0.0f ? to_a : to_q);
-        st = launch_product<false>(large_a, maps, p, d, s);
+        st = launch_product<false>(cut_a, maps, p, d, s);
         if (st != GEMM_OK)
             return st;
 
@@ -1153,7 +1263,7 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
             maps.left = maps.right = a_load;
             maps.left_diag = maps.right_diag = a_diag_load;
             set_stores(maps, to_q);
-            st = launch_product<false>(large_a, maps, p, d, s);
+            st = launch_product<false>(cut_s, maps, p, d, s);
             if (st != GEMM_OK)
                 return st;
         }
@@ -1197,7 +1307,7 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
             p.planes_pitch = l.xp;
             p.alpha = 1.0f / kScaleQ;
         }
-        st = launch_product<true>(large_x, maps, p, d, s);
+        st = launch_product<true>(cut_x, maps, p, d, s);
         if (st != GEMM_OK)
             return st;
     }
