@@ -46,13 +46,9 @@
 #include <cstdint>
 #include <cstring>
 
-#include <cuda_fp16.h>
-
-#include "gemm_internal.h"
+#include "orthogonalize_internal.h"
 #include "pipelined_train.h"
-#include "ptx.cuh"
 #include "tma_ring.cuh"
-#include "vector_io.cuh"
 
 namespace pg {
 
@@ -64,12 +60,6 @@ constexpr int kUmmaK = 16;
 constexpr uint32_t kAtomBytes = 64 * BK * 2;    // 64 columns of an MN-major operand: 8 KiB
 constexpr int kDiagBlock = 256;                 // side of the diagonal blocks that keep the extra plane
 constexpr uint32_t kStagingBytes = 32 * 128;    // per epilogue warp: 32 rows of 128 bytes
-
-// Powers of two the planes are scaled by: the largest magnitudes they must
-// hold under float16's 65504 are X 4, A + (b / 2c) I 8, Q 32 (orthogonalize()
-// refuses coefficients that reach further), and nothing that matters at the
-// other end falls below its 2^-14.
-constexpr float kScaleX = 16384.0f, kScaleA = 8192.0f, kScaleQ = 2048.0f;
 
 // One pair of planes to multiply.  Plane -1 is the diagonal-block plane.
 // `range`: all of K, or the K of this tile's rows or columns.
@@ -225,23 +215,6 @@ __device__ __forceinline__ Blocks tile_blocks(const Product &p, const TileAt &at
     n.lo = rank * n.all / p.ranks;
     n.hi = (rank + 1) * n.all / p.ranks;
     return n;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float a, float b)
-{
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
-{
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-__device__ __forceinline__ float2 unpack_f16(uint32_t w)
-{
-    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
 // An epilogue warp's 4 KiB staging buffers, from which TMA stores move boxes.
@@ -752,11 +725,7 @@ __global__ void __launch_bounds__(Tile<MH, BN, S, Split>::kThreads, 1)
 
 // ------------------------------------------------------------ norm and planes of G
 struct Input {
-    const void *G;
-    int bf16;
-    int m, n, batch;
-    long long ld, batch_pitch; // elements
-    int vec;                   // rows can be read eight elements at a time
+    Matrix g;
     float eps;
     float2 *partial; // [batch][parts]
     int parts;
@@ -767,45 +736,18 @@ struct Input {
 
 constexpr int kNormThreads = 256;
 
-// Eight consecutive elements j .. j+7 of a row of n, zero past its end.
-__device__ __forceinline__ void load8(const Input &p, long long row_at, int j, float (&v)[8])
-{
-    if (p.vec && j + 8 <= p.n) {
-        if (p.bf16) {
-            const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.G) + row_at + j);
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[2 * e] = __uint_as_float(w[e] << 16);
-                v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-            }
-        } else {
-            const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p.G) + row_at + j);
-            const float4 a = q[0], b = q[1];
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = j + e < p.n ? load_f32(p.G, p.bf16, row_at + j + e) : 0.0f;
-    }
-}
-
-// Sums of squares, and of the squares of 2^-96 times the elements for the
-// norm of a G whose squares overflow float32.
+// The sums of squares, one pair of partial sums per CTA.
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(const Input p)
 {
     __shared__ float2 scratch[kNormThreads / 32];
     const int b = blockIdx.y;
-    const unsigned units = static_cast<unsigned>((p.n + 7) / 8);
-    const unsigned total = units * static_cast<unsigned>(p.m);
-    constexpr float kDown = 1.26217744835361889e-29f; // 2^-96
+    const unsigned units = static_cast<unsigned>((p.g.n + 7) / 8);
+    const unsigned total = units * static_cast<unsigned>(p.g.m);
     float s = 0.0f, t = 0.0f;
     for (unsigned u = blockIdx.x * kNormThreads + threadIdx.x; u < total; u += gridDim.x * kNormThreads) {
         const unsigned row = u / units;
         float v[8];
-        load8(p, b * p.batch_pitch + row * p.ld, static_cast<int>(u - row * units) * 8, v);
+        load8(p.g, b * p.g.batch_pitch + row * p.g.ld, static_cast<int>(u - row * units) * 8, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             s = fmaf(v[e], v[e], s);
@@ -855,18 +797,8 @@ __global__ void __launch_bounds__(kNormThreads) planes_kernel(const Input p)
             t += __shfl_xor_sync(0xffffffffu, t, o);
         }
         if (threadIdx.x == 0) {
-            // 1 / (|G|_F + eps) = inv 2^shift; an infinite or NaN norm makes
-            // every element NaN.
-            const bool big = !(s < __int_as_float(0x7f800000));
-            const float norm = big ? sqrtf(t) : sqrtf(s);
-            const float inv = big ? 1.0f / (norm + p.eps * 1.26217744835361889e-29f) : 1.0f / (norm + p.eps);
-            int e = 0;
-            float f = __int_as_float(0x7fc00000);
-            if (norm < __int_as_float(0x7f800000) && inv < __int_as_float(0x7f800000)) {
-                e = ilogbf(inv);
-                f = scalbnf(inv, -e);
-                e += (big ? -96 : 0) + 14; // kScaleX
-            }
+            int e;
+            const float f = split_scale(s, t, p.eps, &e);
             scale[0] = scalbnf(1.0f, e / 2);
             scale[1] = scalbnf(1.0f, e - e / 2);
             if (blockIdx.x == 0 && blockIdx.y == 0)
@@ -875,16 +807,16 @@ __global__ void __launch_bounds__(kNormThreads) planes_kernel(const Input p)
     }
     __syncthreads();
     const float s0 = scale[0], s1 = scale[1];
-    const int r = Tall ? p.n : p.m, c = Tall ? p.m : p.n;
+    const int r = Tall ? p.g.n : p.g.m, c = Tall ? p.g.m : p.g.n;
     const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
     const int ty = threadIdx.x / 8, tx = threadIdx.x % 8 * 8;
-    const long long first = b * p.batch_pitch;
+    const long long first = b * p.g.batch_pitch;
     if constexpr (Tall) {
 #pragma unroll
         for (int h = 0; h < 64; h += 32) {
             float v[8];
             if (j0 + ty + h < c) {
-                load8(p, first + (j0 + ty + h) * p.ld, i0 + tx, v);
+                load8(p.g, first + (j0 + ty + h) * p.g.ld, i0 + tx, v);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -907,7 +839,7 @@ __global__ void __launch_bounds__(kNormThreads) planes_kernel(const Input p)
             for (int e = 0; e < 8; ++e)
                 v[e] = piece[ty + h][tx + e];
         } else {
-            load8(p, first + i * p.ld, j0 + tx, v);
+            load8(p.g, first + i * p.g.ld, j0 + tx, v);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -997,39 +929,6 @@ int encode_column_groups(CUtensorMap *map, const Planes &m, uint32_t columns)
     return encode_tensor_map(map, kElement16, m.base, 4, dims, pitches, box, 128);
 }
 
-// `overlap`: the kernel may start while the one before it ends (it calls
-// grid_wait()); `cluster`: CTAs per cluster.
-template <class Kernel, class... Args>
-int launch(Kernel kernel, dim3 grid, int threads, int smem, bool overlap, int cluster, cudaStream_t s,
-           const Args &...args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2] = {};
-    unsigned n = 0;
-    if (overlap) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n++].val.programmaticStreamSerializationAllowed = 1;
-    }
-    if (cluster > 1) {
-        attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
-        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
-        ++n;
-    }
-    cfg.attrs = attr;
-    cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
-}
-
-struct Device {
-    int index, sms;
-    unsigned long long ctx;
-};
-
 template <int MH, int BN, int S, bool RightMN, bool Split>
 int launch_product_t(const Maps &maps, const Product &p, const Device &d, cudaStream_t s)
 {
@@ -1092,19 +991,6 @@ int launch_product(const Cut &cut, const Maps &maps, Product p, const Device &d,
     return cut.ranks > 1 ? launch_product_t<1, 128, 4, RightMN, true>(maps, p, d, s)
                          : launch_product_t<1, 128, 4, RightMN, false>(maps, p, d, s);
 }
-
-struct Call {
-    int batch, m, n;
-    const void *G;
-    long long ldg, g_batch;
-    int dtype;
-    void *out;
-    long long ldo, o_batch;
-    int out_dtype;
-    int steps;
-    const float *coefficients;
-    float eps;
-};
 
 int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigned int *status, cudaStream_t s)
 {
@@ -1178,12 +1064,8 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
 
     // Norm and the first iterate.  A bfloat16 G is exact in one plane.
     const bool exact_input = call.dtype == GEMM_DTYPE_BF16;
-    Input in{call.G, call.dtype == GEMM_DTYPE_BF16, call.m, call.n, nb, call.ldg, call.g_batch, 0, call.eps,
-             reinterpret_cast<float2 *>(ws + l.partial), l.parts, f, static_cast<__half *>(x[0].base), l.xp,
-             exact_input ? 1 : l.xp, l.cp};
-    const uint64_t gs = call.dtype == GEMM_DTYPE_F32 ? 4 : 2;
-    in.vec = (reinterpret_cast<uintptr_t>(call.G) & 15u) == 0 && (call.ldg * gs) % 16 == 0 &&
-             (nb == 1 || (call.g_batch * gs) % 16 == 0);
+    const Input in{call.matrix(), call.eps, reinterpret_cast<float2 *>(ws + l.partial), l.parts, f,
+                   static_cast<__half *>(x[0].base), l.xp, exact_input ? 1 : l.xp, l.cp};
     st = launch(norm_kernel, dim3(l.parts, nb), kNormThreads, 0, false, 1, s, in);
     if (st != GEMM_OK)
         return st;
@@ -1375,7 +1257,8 @@ int orthogonalize_workspace(int batch, int m, int n, int out_dtype, size_t *byte
     const int st = orth::check_sizes(batch, m, n);
     if (st != GEMM_OK)
         return st;
-    *bytes = batch == 0 || m == 0 || n == 0 ? 0 : orth::make_layout(batch, m, n, out_dtype, device_sms()).total;
+    const bool none = batch == 0 || m == 0 || n == 0 || orth::fits_small(m, n, out_dtype);
+    *bytes = none ? 0 : orth::make_layout(batch, m, n, out_dtype, device_sms()).total;
     return GEMM_OK;
 }
 
@@ -1410,13 +1293,15 @@ int orthogonalize(int batch, int m, int n, const void *G, long long ldg, long lo
     if (empty)
         return GEMM_OK;
     const orth::Device d{dev, device_sms(), current_context_id()};
-    const orth::Layout l = orth::make_layout(batch, m, n, out_dtype, d.sms);
-    if (!workspace || workspace_bytes < l.total)
-        return GEMM_ERR_INVALID_ARG;
     unsigned int *status = device_status_word(dev, d.ctx);
     if (!status)
         return GEMM_ERR_CUDA;
     const orth::Call call{batch, m, n, G, ldg, g_batch, dtype, out, ldo, o_batch, out_dtype, steps, coefficients, eps};
+    if (orth::fits_small(m, n, out_dtype))
+        return orth::run_small(call, d, status, static_cast<cudaStream_t>(stream));
+    const orth::Layout l = orth::make_layout(batch, m, n, out_dtype, d.sms);
+    if (!workspace || workspace_bytes < l.total)
+        return GEMM_ERR_INVALID_ARG;
     return orth::run(call, l, static_cast<uint8_t *>(workspace), d, status, static_cast<cudaStream_t>(stream));
 }
 

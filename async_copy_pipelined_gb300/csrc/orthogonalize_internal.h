@@ -1,0 +1,162 @@
+// What the orthogonalisation's kernels share: how G is read and normalised,
+// how values are kept as float16 planes, and the call as its entry point
+// (orthogonalize.cu) hands it on.
+#pragma once
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_fp16.h>
+
+#include "gemm_internal.h"
+#include "pipelined_train.h"
+#include "ptx.cuh"
+#include "tma_ring.cuh"
+#include "vector_io.cuh"
+
+namespace pg {
+
+namespace orth {
+
+// Powers of two the planes are scaled by: the largest magnitudes they must
+// hold under float16's 65504 are X 4, A + (b / 2c) I 8, Q 32 (orthogonalize()
+// refuses coefficients that reach further), and nothing that matters at the
+// other end falls below its 2^-14.
+constexpr float kScaleX = 16384.0f, kScaleA = 8192.0f, kScaleQ = 2048.0f;
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float2 unpack_f16(uint32_t w)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// A batch of row-major matrices to read.
+struct Matrix {
+    const void *G;
+    int bf16;
+    int m, n;
+    long long ld, batch_pitch; // elements
+    int vec;                   // rows can be read eight elements at a time
+};
+
+// Eight consecutive elements j .. j+7 of a row of n, zero past its end.
+__device__ __forceinline__ void load8(const Matrix &p, long long row_at, int j, float (&v)[8])
+{
+    if (p.vec && j + 8 <= p.n) {
+        if (p.bf16) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.G) + row_at + j);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[2 * e] = __uint_as_float(w[e] << 16);
+                v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+            }
+        } else {
+            const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p.G) + row_at + j);
+            const float4 a = q[0], b = q[1];
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = j + e < p.n ? load_f32(p.G, p.bf16, row_at + j + e) : 0.0f;
+    }
+}
+
+// Squares are summed of the elements, and of 2^-96 times them for the norm of
+// a G whose squares overflow float32.
+constexpr float kDown = 1.26217744835361889e-29f; // 2^-96
+
+// From the two sums: f and the power of two e with 2^e f = kScaleX / (|G|_F +
+// eps), f in [1, 2).  An infinite or NaN norm makes f, and so every element
+// that comes of it, NaN.
+__device__ __forceinline__ float split_scale(float s, float t, float eps, int *e)
+{
+    const float inf = __int_as_float(0x7f800000);
+    const bool big = !(s < inf);
+    const float norm = big ? sqrtf(t) : sqrtf(s);
+    const float inv = big ? 1.0f / (norm + eps * kDown) : 1.0f / (norm + eps);
+    *e = 0;
+    if (!(norm < inf && inv < inf))
+        return __int_as_float(0x7fc00000);
+    const int k = ilogbf(inv);
+    *e = k + (big ? -96 : 0) + 14; // kScaleX
+    return scalbnf(inv, -k);
+}
+
+// `overlap`: the kernel may start while the one before it ends (it calls
+// grid_wait()); `cluster`: CTAs per cluster.
+template <class Kernel, class... Args>
+int launch(Kernel kernel, dim3 grid, int threads, int smem, bool overlap, int cluster, cudaStream_t s,
+           const Args &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2] = {};
+    unsigned n = 0;
+    if (overlap) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+struct Device {
+    int index, sms;
+    unsigned long long ctx;
+};
+
+struct Call {
+    int batch, m, n;
+    const void *G;
+    long long ldg, g_batch;
+    int dtype;
+    void *out;
+    long long ldo, o_batch;
+    int out_dtype;
+    int steps;
+    const float *coefficients;
+    float eps;
+
+    Matrix matrix() const
+    {
+        const long long size = dtype == GEMM_DTYPE_BF16 ? 2 : 4;
+        const bool vec = (reinterpret_cast<uintptr_t>(G) & 15u) == 0 && (ldg * size) % 16 == 0 &&
+                         (batch == 1 || (g_batch * size) % 16 == 0);
+        return Matrix{G, dtype == GEMM_DTYPE_BF16, m, n, ldg, g_batch, vec};
+    }
+};
+
+
+// bfloat16 results of matrices whose shorter side is at most 128 and whose
+// longer one a cluster of eight CTAs holds (orthogonalize_small.cu).
+bool fits_small(int m, int n, int out_dtype);
+int run_small(const Call &call, const Device &d, unsigned int *status, cudaStream_t s);
+
+} // namespace orth
+
+} // namespace pg

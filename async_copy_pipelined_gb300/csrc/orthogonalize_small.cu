@@ -1,0 +1,505 @@
+// The orthogonalisation of small matrices in one kernel: everything stays in
+// shared and tensor memory from G to the result.
+//
+// The iteration is that of orthogonalize.cu, bfloat16 results only, for
+// matrices whose shorter side r is at most 128.  There a product takes a
+// microsecond and the rest of a launch, a round through L2 and the wait for the
+// kernel before take seven.  One CTA holds up to 256 columns of X (two
+// float16 planes, 128 KiB), and A and then Q in two planes (64 KiB); 1, 2, 4
+// or 8 CTAs, a cluster, hold a matrix.  The square and Q X need no exchange:
+// every CTA has all of A.  X X^T is summed over the CTAs' columns, each rank
+// adding the others' partial sums of its part in rank order and sending the
+// finished planes to all.
+//
+// X lies as 64-column blocks of 128 rows of 128 bytes in the 128-byte swizzle:
+// K-major for X X^T, and the same bytes are the MN-major right operand of Q X.
+//
+// Measured on GB300 (microseconds a call, against orthogonalize.cu's kernels):
+// see the table at fits_small().
+#include <algorithm>
+
+#include "orthogonalize_internal.h"
+
+namespace pg {
+
+namespace orth {
+
+constexpr int kSmallRows = 128;
+constexpr int kSlab = 256;     // columns of X that a CTA holds
+constexpr int kMaxRanks = 8;
+constexpr int kSmallThreads = 256;
+constexpr int kSmallSteps = 32;
+constexpr uint32_t kColumnBlock = kSmallRows * 128; // 64 columns: 16 KiB
+constexpr uint32_t kUnit = 32 * 64 * 4;             // a warp's share of a 128 x 128 sum
+
+// Shared memory, from a 1024-byte boundary.
+constexpr uint32_t kX0 = 0, kX1 = 4 * kColumnBlock;                    // X's planes
+constexpr uint32_t kA0 = 8 * kColumnBlock, kA1 = 10 * kColumnBlock;    // A's, then Q's
+constexpr uint32_t kReceive = kA0;                                     // where the other ranks' sums arrive
+constexpr uint32_t kSmallSmem = 12 * kColumnBlock + 1024;
+static_assert(8 * kUnit <= 4 * kColumnBlock, "the sums fit where A and Q are not yet");
+
+struct Small {
+    Matrix g;
+    int r, c, tall;
+    int ranks, blocks; // CTAs of a matrix; 64-column blocks that each holds
+    void *out;
+    long long ldo, out_batch;
+    int out_vec; // rows of out can be written eight elements at a time
+    int steps;
+    float eps;
+    unsigned int *status;
+    unsigned long long wait_limit_ns;
+    int withhold;
+    float coefficients[3 * kSmallSteps];
+};
+
+constexpr uint32_t instruction(int n, bool right_mn)
+{
+    return (1u << 4) | (right_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(kSmallRows >> 4) << 24);
+}
+
+// 64 columns of this lane's row as one plane: in the 128-byte swizzle to
+// `row` (the row's 128 bytes of a column block), what it leaves over in v.
+__device__ __forceinline__ void make_plane(unsigned long long (&v)[32], uint32_t (&w)[32])
+{
+    const unsigned long long minus = pair(-1.0f, -1.0f);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        float lo, hi;
+        split(v[j], lo, hi);
+        w[j] = pack_f16(lo, hi);
+        const float2 kept = unpack_f16(w[j]);
+        v[j] = fma2(pair(kept.x, kept.y), minus, v[j]);
+    }
+}
+
+__device__ __forceinline__ void store_plane(uint32_t row, int lane, const uint32_t (&w)[32], bool remote)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t at = row + static_cast<uint32_t>((j ^ (lane & 7)) << 4);
+        if (remote)
+            st_cluster_v4(at, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        else
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(w[4 * j]), "r"(w[4 * j + 1]),
+                         "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
+                         : "memory");
+    }
+}
+
+__global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_constant__ Small p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2];
+    __shared__ uint32_t tmem_slot;
+    __shared__ float2 warp_sums[kSmallThreads / 32];
+    __shared__ float2 rank_sums[kMaxRanks];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = align_smem(raw, 1024); // the same offset in every CTA of the cluster
+    const uint32_t done = smem_u32(&bars[0]), drained = smem_u32(&bars[1]);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = p.ranks > 1 ? static_cast<int>(cluster_cta_rank()) : 0;
+    const int b = static_cast<int>(blockIdx.x) / p.ranks;
+    const int width = p.blocks * 64, col0 = rank * width; // this CTA's columns of X
+    const int quarter = warp & 3, half = warp >> 2;       // of the accumulators' rows and columns
+    const int row = quarter * 32 + lane;
+    auto sync = [&]() {
+        if (p.ranks > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+    };
+
+    if (threadIdx.x == 0) {
+        mbar_init(done, 1);
+        mbar_init(drained, 1);
+        fence_barrier_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_u32(&tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    sync(); // also: every CTA of the cluster has started
+    tc_fence_after_sync();
+    const uint32_t tmem = *static_cast<volatile uint32_t *>(&tmem_slot);
+
+    // ------------------------------------------------ G's columns, twice
+    // Eight elements at a time: of a wide G a row's, lane l columns 8 l ..; of
+    // a tall one (X is its transpose) a column of X, neighbouring lanes'
+    // columns neighbours, so that the transposed stores do not collide.
+    const long long g0 = b * p.g.batch_pitch;
+    auto visit = [&](auto take) {
+        float v[8];
+        if (!p.tall) {
+            const int j = lane * 8;
+            if (j < width)
+                for (int i = warp; i < kSmallRows; i += kSmallThreads / 32) {
+                    const bool in = i < p.r && col0 + j < p.c;
+                    if (in)
+                        load8(p.g, g0 + i * p.g.ld, col0 + j, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = in ? v[e] : 0.0f;
+                    take(v, i, j);
+                }
+        } else {
+            for (int u = warp; u < p.blocks * 2 * (kSmallRows / 8); u += kSmallThreads / 32) {
+                const int i = u % (kSmallRows / 8) * 8, j = u / (kSmallRows / 8) * 32 + lane;
+                const bool in = i < p.r && col0 + j < p.c;
+                if (in)
+                    load8(p.g, g0 + (col0 + j) * p.g.ld, i, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = in ? v[e] : 0.0f;
+                take(v, i, j);
+            }
+        }
+    };
+    float s = 0.0f, t = 0.0f;
+    visit([&](const float (&v)[8], int, int) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            s = fmaf(v[e], v[e], s);
+            const float d = v[e] * kDown;
+            t = fmaf(d, d, t);
+        }
+    });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        t += __shfl_xor_sync(0xffffffffu, t, o);
+    }
+    if (lane == 0)
+        warp_sums[warp] = make_float2(s, t);
+    __syncthreads();
+    if (threadIdx.x < p.ranks) { // this CTA's sums to rank threadIdx.x
+        s = t = 0.0f;
+        for (int w = 0; w < kSmallThreads / 32; ++w) {
+            s += warp_sums[w].x;
+            t += warp_sums[w].y;
+        }
+        const uint32_t slot = smem_u32(&rank_sums[rank]);
+        if (p.ranks > 1)
+            st_cluster_v2(map_to_cta(slot, threadIdx.x), __float_as_uint(s), __float_as_uint(t));
+        else
+            rank_sums[0] = make_float2(s, t);
+    }
+    sync();
+    s = t = 0.0f;
+    for (int k = 0; k < p.ranks; ++k) {
+        s += rank_sums[k].x;
+        t += rank_sums[k].y;
+    }
+    int e2;
+    const float f = split_scale(s, t, p.eps, &e2);
+    const float s0 = scalbnf(1.0f, e2 / 2), s1 = scalbnf(1.0f, e2 - e2 / 2);
+    const bool exact = p.g.bf16 != 0; // one plane holds a bfloat16 G
+    visit([&](const float (&v)[8], int i, int j) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] = v[e] * s0 * s1;
+        for (int q = 0; q < (exact ? 1 : 2); ++q) {
+            const uint32_t plane = base + (q == 0 ? kX0 : kX1) + static_cast<uint32_t>(j / 64) * kColumnBlock;
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                w[e] = pack_f16(x[2 * e], x[2 * e + 1]);
+                const float2 kept = unpack_f16(w[e]);
+                x[2 * e] -= kept.x;
+                x[2 * e + 1] -= kept.y;
+            }
+            if (!p.tall) {
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(
+                                 plane + static_cast<uint32_t>(i * 128 + ((((j % 64) / 8) ^ (i & 7)) << 4))),
+                             "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                             : "memory");
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(
+                                     plane + static_cast<uint32_t>((i + e) * 128 + ((((j % 64) / 8) ^ e) << 4) +
+                                                                   (j % 8) * 2)),
+                                 "h"(static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1))))
+                                 : "memory");
+            }
+        }
+    });
+
+    // ------------------------------------------------ the iteration
+    uint32_t parity = 0;
+    int product = 0;
+    bool failed = false;
+    // What the threads have written is there for the tensor core; one thread
+    // issues the product, all wait for it.  After a wait that ran out nobody
+    // waits again and the barriers stay matched.
+    auto multiply = [&](auto issue) {
+        fence_proxy_async_smem();
+        tc_fence_before_sync();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            tc_fence_after_sync();
+            issue();
+            if (product != p.withhold) // test hook: this product is never announced
+                mma_commit(done);
+        }
+        ++product;
+        __syncwarp();
+        if (!failed && !mbar_wait_bounded(done, parity, p.wait_limit_ns)) {
+            failed = true;
+            record_error(p.status, kErrFamilyOrthogonalize | kErrRoleMma);
+        }
+        parity ^= 1u;
+        tc_fence_after_sync();
+        __syncwarp();
+    };
+    // 64 columns of this thread's row of the accumulator at `column`.
+    auto read = [&](int column, unsigned long long (&v)[32]) {
+        uint32_t r0[32], r1[32];
+        const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(column);
+        tmem_ld_32x32b_x32(at, r0);
+        tmem_ld_32x32b_x32(at + 32u, r1);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            v[j] = pair(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]));
+            v[16 + j] = pair(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]));
+        }
+    };
+    // v alpha + diag I, for columns half * 64 .. of a 128 x 128 matrix.
+    auto scale = [&](unsigned long long (&v)[32], float alpha, float diag) {
+        const unsigned long long a = pair(alpha, alpha);
+        const int at = row < p.r ? row - half * 64 : -1; // where the diagonal is among these columns
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            v[j] = fma2(v[j], a, pair(2 * j == at ? diag : 0.0f, 2 * j + 1 == at ? diag : 0.0f));
+    };
+    const int k_blocks = p.r > 64 ? 2 : 1; // of A and Q
+    auto square_pass = [&](uint32_t left, uint32_t right, bool first) {
+        for (int kb = 0; kb < k_blocks; ++kb)
+            for (int ks = 0; ks < 4; ++ks) {
+                const uint32_t at = static_cast<uint32_t>(kb) * kColumnBlock + static_cast<uint32_t>(ks) * 32u;
+                mma_f16_ss(tmem, smem_desc_sw128(base + left + at, 16, 1024),
+                           smem_desc_sw128(base + right + at, 16, 1024), instruction(128, false),
+                           !first || kb != 0 || ks != 0 ? 1u : 0u);
+            }
+    };
+    constexpr int kResult = 128; // accumulator of Q X, beside that of X X^T and the square
+    auto result_pass = [&](uint32_t left, uint32_t right, bool first) {
+        for (int kb = 0; kb < k_blocks; ++kb)
+            for (int ks = 0; ks < 4; ++ks)
+                mma_f16_ss(tmem + kResult,
+                           smem_desc_sw128(base + left + static_cast<uint32_t>(kb) * kColumnBlock +
+                                               static_cast<uint32_t>(ks) * 32u, 16, 1024),
+                           smem_desc_sw128(base + right + static_cast<uint32_t>(kb * 64 + ks * 16) * 128u,
+                                           kColumnBlock, 1024),
+                           instruction(width, true), !first || kb != 0 || ks != 0 ? 1u : 0u);
+    };
+
+    for (int step = 0; step < p.steps; ++step) {
+        const float ca = p.coefficients[3 * step], cb = p.coefficients[3 * step + 1],
+                    cc = p.coefficients[3 * step + 2];
+        const bool first = step == 0, last = step == p.steps - 1;
+        const float fs = first ? f : 1.0f;
+        unsigned long long v[32];
+        uint32_t w[32];
+
+        // X X^T, over all ranks' columns.
+        multiply([&]() {
+            for (int kb = 0; kb < p.blocks; ++kb)
+                for (int ks = 0; ks < 4; ++ks) {
+                    const uint64_t d = smem_desc_sw128(
+                        base + kX0 + static_cast<uint32_t>(kb) * kColumnBlock + static_cast<uint32_t>(ks) * 32u, 16, 1024);
+                    mma_f16_ss(tmem, d, d, instruction(128, false), kb != 0 || ks != 0 ? 1u : 0u);
+                }
+        });
+        read(half * 64, v);
+        const int unit = quarter * 2 + half, each = 8 / p.ranks, owner = unit / each;
+        if (p.ranks > 1) {
+            const uint32_t slots = base + kReceive + static_cast<uint32_t>(unit % each * p.ranks) * kUnit;
+            cluster_sync(); // no rank still multiplies by the Q that lies there
+            if (owner != rank) {
+                const uint32_t to = map_to_cta(slots + static_cast<uint32_t>(rank) * kUnit,
+                                               static_cast<uint32_t>(owner)) + static_cast<uint32_t>(lane) * 16u;
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    float q0, q1, q2, q3;
+                    split(v[j], q0, q1);
+                    split(v[j + 1], q2, q3);
+                    st_cluster_v4(to + static_cast<uint32_t>(j) * 256u, __float_as_uint(q0), __float_as_uint(q1),
+                                  __float_as_uint(q2), __float_as_uint(q3));
+                }
+            }
+            cluster_sync();
+            if (owner == rank) {
+                for (int src = 0; src < p.ranks; ++src) {
+                    if (src == rank)
+                        continue;
+                    const uint8_t *from = smem_raw + (slots - raw) + src * kUnit + lane * 16;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float4 q = *reinterpret_cast<const float4 *>(from + j * 256);
+                        v[j] = add2(v[j], pair(q.x, q.y));
+                        v[j + 1] = add2(v[j + 1], pair(q.z, q.w));
+                    }
+                }
+            }
+            cluster_sync(); // the sums have been taken: A (or Q) may lie there
+        }
+        if (cc != 0.0f)
+            scale(v, kScaleA / (kScaleX * kScaleX) * fs * fs, kScaleA * (cb / (2.0f * cc)));
+        else
+            scale(v, kScaleQ * cb / (kScaleX * kScaleX) * fs * fs * fs, kScaleQ * ca * fs);
+        const uint32_t row_at = static_cast<uint32_t>(half) * kColumnBlock + static_cast<uint32_t>(row) * 128u;
+        if (owner == rank || p.ranks == 1) {
+            for (int q = 0; q < 2; ++q) {
+                make_plane(v, w);
+                const uint32_t to = base + (q == 0 ? kA0 : kA1) + row_at;
+                if (p.ranks == 1)
+                    store_plane(to, lane, w, false);
+                else
+                    for (int k = 0; k < p.ranks; ++k)
+                        store_plane(map_to_cta(to, static_cast<uint32_t>(k)), lane, w, true);
+            }
+        }
+        if (p.ranks > 1)
+            cluster_sync();
+
+        if (cc != 0.0f) {
+            // The square, in every rank, and Q in A's place.
+            multiply([&]() {
+                square_pass(kA1, kA0, true);
+                square_pass(kA0, kA1, false);
+                square_pass(kA0, kA0, false);
+            });
+            read(half * 64, v);
+            scale(v, kScaleQ * cc / (kScaleA * kScaleA) * fs,
+                  kScaleQ * static_cast<float>(ca - static_cast<double>(cb) * cb / (4.0 * cc)) * fs);
+            for (int q = 0; q < 2; ++q) {
+                make_plane(v, w);
+                store_plane(base + (q == 0 ? kA0 : kA1) + row_at, lane, w, false);
+            }
+        }
+
+        // Q X: this rank's columns, in X's place or to the result.
+        multiply([&]() {
+            result_pass(kA1, kX0, true);
+            if (!last && !(first && exact))
+                result_pass(kA0, kX1, false);
+            result_pass(kA0, kX0, false);
+        });
+        for (int k = 0; k < 2; ++k) {
+            const int block = half * 2 + k;
+            if (block >= p.blocks)
+                break; // warp-uniform
+            read(kResult + block * 64, v);
+            const float alpha = last ? 1.0f / (kScaleQ * kScaleX) : 1.0f / kScaleQ;
+            const unsigned long long a2 = pair(alpha, alpha);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                v[j] = mul2(v[j], a2);
+            if (!last) {
+                for (int q = 0; q < 2; ++q) {
+                    make_plane(v, w);
+                    store_plane(base + (q == 0 ? kX0 : kX1) + static_cast<uint32_t>(block) * kColumnBlock +
+                                    static_cast<uint32_t>(row) * 128u, lane, w, false);
+                }
+            } else if (row < p.r) {
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + b * p.out_batch;
+                const int j0 = col0 + block * 64;
+                if (p.tall) { // neighbouring lanes write neighbours
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) {
+                        float lo, hi;
+                        split(v[j / 2], lo, hi);
+                        if (j0 + j < p.c)
+                            out[(j0 + j) * p.ldo + row] = __float2bfloat16_rn(j & 1 ? hi : lo);
+                    }
+                } else {
+                    __nv_bfloat16 *o = out + row * p.ldo + j0;
+#pragma unroll
+                    for (int j = 0; j < 64; j += 8) {
+                        float q[8];
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2)
+                            split(v[(j + e) / 2], q[e], q[e + 1]);
+                        if (p.out_vec && j0 + j + 8 <= p.c) {
+                            *reinterpret_cast<uint4 *>(o + j) =
+                                make_uint4(pack_bf16(q[0], q[1]), pack_bf16(q[2], q[3]), pack_bf16(q[4], q[5]),
+                                           pack_bf16(q[6], q[7]));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (j0 + j + e < p.c)
+                                    o[j + e] = __float2bfloat16_rn(q[e]);
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    // Every product has finished before tensor memory is freed, and no rank
+    // leaves while another may still write to it.
+    if (threadIdx.x == 0) {
+        mma_commit(drained);
+        if (!mbar_wait_bounded(drained, 0, p.wait_limit_ns))
+            record_error(p.status, kErrFamilyOrthogonalize | kErrRoleDrain);
+    }
+    __syncwarp();
+    tc_fence_before_sync();
+    sync();
+    tc_fence_after_sync();
+    if (warp == 0)
+        tmem_dealloc(tmem, 512);
+}
+
+// CTAs of a matrix whose longer side is c, and 64-column blocks of each.
+static int ranks_for(int c, int *blocks)
+{
+    int ranks = 1;
+    while (ranks < kMaxRanks && c > ranks * kSlab)
+        ranks *= 2;
+    *blocks = (c + 64 * ranks - 1) / (64 * ranks);
+    return ranks;
+}
+
+bool fits_small(int m, int n, int out_dtype)
+{
+    const int r = std::min(m, n), c = std::max(m, n);
+    return out_dtype == GEMM_DTYPE_BF16 && r <= kSmallRows && c <= kMaxRanks * kSlab;
+}
+
+int run_small(const Call &call, const Device &d, unsigned int *status, cudaStream_t s)
+{
+    Small p = {};
+    p.g = call.matrix();
+    p.r = std::min(call.m, call.n);
+    p.c = std::max(call.m, call.n);
+    p.tall = call.m > call.n;
+    p.ranks = ranks_for(p.c, &p.blocks);
+    p.out = call.out;
+    p.ldo = call.ldo;
+    p.out_batch = call.o_batch;
+    p.out_vec = (reinterpret_cast<uintptr_t>(call.out) & 15u) == 0 && call.ldo % 8 == 0 &&
+                (call.batch == 1 || call.o_batch % 8 == 0);
+    p.steps = call.steps;
+    p.eps = call.eps;
+    p.status = status;
+    p.wait_limit_ns = call_wait_limit_ns();
+    p.withhold = call_withhold();
+    for (int k = 0; k < 3 * call.steps; ++k)
+        p.coefficients[k] = call.coefficients[k];
+    static std::atomic<unsigned long long> limit_set[kMaxDevices];
+    if (ensure_smem_limit(small_kernel, kSmallSmem, d.index, d.ctx, limit_set) != GEMM_OK)
+        return GEMM_ERR_CUDA;
+    return launch(small_kernel, dim3(static_cast<unsigned>(call.batch * p.ranks)), kSmallThreads, kSmallSmem, false,
+                  p.ranks, s, p);
+}
+
+} // namespace orth
+
+} // namespace pg

@@ -274,6 +274,11 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_
                  : "memory");
 }
 
+__device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_t b)
+{
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};\n" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
 // Record the first error of this launch sequence in the device status word.
 __device__ __forceinline__ void record_error(unsigned int *status, unsigned int code)
 {

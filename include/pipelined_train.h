@@ -142,7 +142,9 @@ int orthogonalize(int batch, int m, int n,
                   void *stream);
 
 /* Bytes orthogonalize needs for these sizes on the current device (a 152-SM
- * part where no device can be asked). */
+ * part where no device can be asked).  None for a bfloat16 result of small
+ * matrices (a side of at most 128 and the other at most 2048), which stay on
+ * chip; workspace may then be NULL. */
 int orthogonalize_workspace(int batch, int m, int n, int out_dtype, size_t *bytes);
 
 #ifdef __cplusplus

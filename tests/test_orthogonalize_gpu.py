@@ -285,3 +285,62 @@ def test_a_wait_that_runs_out_is_reported():
     assert status == 6 and detail & 0xFF == 7
     assert (pg.orthogonalize(g) == want).all()
     _check_status()
+
+
+@pytest.mark.parametrize("m,n", [(128, 128), (128, 256), (127, 257), (100, 511), (512, 90), (65, 700), (64, 1024),
+                                 (1025, 64), (120, 1500), (128, 2048), (2048, 128), (128, 2049), (3, 2000), (1, 64),
+                                 (1500, 2), (40, 1)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_short_side(m, n, dtype):
+    """A side of at most 128: one CTA or a cluster holds the matrix."""
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    for kind in ("flat", "decay"):
+        g = torch.stack([_gradient(m, n, kind, m + n + b, scale=10.0 ** (2 * b)) for b in range(3)])
+        g = g.to(_torch_dtype(dtype))
+        o = pg.orthogonalize(g, dtype=torch.bfloat16)
+        for b in range(3):
+            assert _rel(o[b], _exact(g[b])) <= _tol("bf16", g[b]), (kind, b)
+        assert torch.equal(o, pg.orthogonalize(g, dtype=torch.bfloat16))
+    _check_status()
+
+
+@pytest.mark.parametrize("m,n", [(60, 90), (90, 700), (700, 90)])
+def test_a_short_side_in_place_strided_and_not_finite(m, n):
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    g = torch.stack([_gradient(m, n, "flat", b) for b in range(6)]).bfloat16()
+    want = pg.orthogonalize(g)
+    for pad, offset in ((0, 1), (8, 8), (3, 0)):
+        buf = torch.full((offset + 6 * m * (n + pad),), 77.0, dtype=torch.bfloat16, device="cuda")
+        view = buf[offset:].view(6, m, n + pad)[:, :, :n]
+        view.copy_(g)
+        assert torch.equal(pg.orthogonalize(view), want)
+        pg.orthogonalize(view, view)
+        assert torch.equal(view, want)
+        view.fill_(77.0)
+        assert (buf == 77.0).all()
+    g[1] = 0.0
+    g[2, m - 1, n - 1] = float("nan")
+    g[4, 0, 0] = float("inf")
+    o = pg.orthogonalize(g)
+    assert (o[1] == 0).all() and o[2].isnan().all() and o[4].isnan().all()
+    assert all(torch.equal(o[k], want[k]) for k in (0, 3, 5))
+    _check_status()
+
+
+@pytest.mark.parametrize("m,n", [(100, 200), (100, 900)])
+def test_a_short_side_reports_a_wait_that_runs_out(m, n):
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    g = _gradient(m, n, "flat", 1).bfloat16()
+    want = pg.orthogonalize(g)
+    try:
+        pg.testing_set_hooks(20_000_000, 4)
+        pg.orthogonalize(g)
+    finally:
+        pg.testing_set_hooks()
+    status, detail = pg.device_status()
+    assert status == 6 and detail & 0xFF == 7
+    assert torch.equal(pg.orthogonalize(g), want)
+    _check_status()
