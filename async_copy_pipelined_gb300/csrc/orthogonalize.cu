@@ -117,9 +117,10 @@ struct Product {
 
 // Tile of MH x 128 rows by BN columns, S ring stages.  The 256 x 256 tile
 // fills tensor memory with one accumulator and has each of its eight epilogue
-// warps take a quarter's 256 columns in turn; the 128 x 128 tile has four
-// accumulators and each warp takes 64 columns at once, so that it can also
-// sum a tile's accumulators in registers (Product.fine).
+// warps take a quarter's 256 columns in turn; the 128-row tiles, of 128 or 192
+// columns, have four or two accumulators and each warp takes 64 columns at
+// once, so that it can also sum a tile's accumulators in registers
+// (Product.fine).
 //
 // Split: where the 128 x 128 tiles are fewer than half the SMs, a cluster of
 // 2, 4 or 8 CTAs shares a tile's K blocks, each multiplying its run of them.
@@ -133,8 +134,8 @@ struct Tile {
     static constexpr uint32_t kStageBytes = kLeftBytes + BN * BK * 2;
     static constexpr int kAccBufs = 512 / (MH * BN);
     static constexpr uint32_t kTmemCols = 512;
-    static constexpr int kEpiWarps = 8;
-    static constexpr int kEpiCols = MH * BN / 2; // columns per epilogue warp
+    static constexpr int kEpiCols = MH == 2 ? BN : 64; // columns per epilogue warp
+    static constexpr int kEpiWarps = 4 * MH * BN / kEpiCols;
     static constexpr int kThreads = (2 + kEpiWarps) * 32;
     static constexpr uint32_t kUnitBytes = 32 * 64 * 4;
     static constexpr uint32_t kReceiveBytes = Split ? kEpiWarps * kUnitBytes : 0;
@@ -221,7 +222,7 @@ __device__ __forceinline__ Blocks tile_blocks(const Product &p, const TileAt &at
 // The one of its own is written again when the store before has read it.  In
 // a CTA's last tile the ring is idle and lends each warp kLentBufs more, so
 // that no write waits.
-constexpr int kLentBufs = 4;
+constexpr int kLentBufs = 3;
 
 struct Staging {
     uint32_t own, lent; // first addresses; lent 0: not now
@@ -943,41 +944,75 @@ int launch_product_t(const Maps &maps, const Product &p, const Device &d, cudaSt
     return launch(kernel, dim3(grid), T::kThreads, T::kSmem, true, p.ranks, s, maps, p);
 }
 
-// How a product is cut: tiles of 256 x 256 or 128 x 128, the latter shared by
-// `ranks` CTAs.
+// How a product is cut: tiles of 256 x 256, 128 x 192 (Q X only) or 128 x
+// 128, the last shared by `ranks` CTAs.
 struct Cut {
-    bool large;
-    int ranks;
+    int rows, cols, ranks;
 };
 
-// By the time of one round of tiles, in microseconds measured on GB300: a K
-// block takes the 256 x 256 tile 0.65 and the 128 x 128 tile 0.34 (64 and 32
-// KiB at the 64 bytes a clock that an SM takes in), a K block with an
-// accumulator of its own 0.45; storing a tile takes about 4.5 and 1.5, an
-// exchange between ranks 1.  Ranks only where all tiles run at once.
-Cut choose_cut(bool symmetric, int rows, int cols, int batch, int k_blocks, bool fine, int sms)
+// Clusters of `ranks` CTAs with the split kernel's shared memory that run at
+// once: 76, 36 and 15 of 2, 4 and 8 on GB300, whose GPCs do not hold whole
+// numbers of the larger ones.
+int cluster_room(int ranks, const Device &d)
 {
-    auto tiles = [&](int side) {
-        return static_cast<long long>(tiles_of(symmetric, (rows + side - 1) / side, (cols + side - 1) / side)) * batch;
+    static std::atomic<int> known[kMaxDevices][4];
+    const int at = ranks == 2 ? 1 : ranks == 4 ? 2 : 3;
+    const int have = d.index >= 0 && d.index < kMaxDevices ? known[d.index][at].load() : 0;
+    if (have > 0)
+        return have;
+    using T = Tile<1, 128, 4, true>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(d.sms / ranks * ranks));
+    cfg.blockDim = dim3(T::kThreads);
+    cfg.dynamicSmemBytes = T::kSmem;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(ranks);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    auto *kernel = product_kernel<1, 128, 4, true, true>;
+    int n = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    if (d.index >= 0 && d.index < kMaxDevices)
+        known[d.index][at].store(n);
+    return n;
+}
+
+// By the time of one round of tiles, in microseconds measured on GB300: a K
+// block takes the 256 x 256 tile 0.65, the 128 x 192 tile 0.43 and the 128 x
+// 128 tile 0.34 (64, 40 and 32 KiB at the 64 bytes a clock that an SM takes
+// in), with an accumulator of its own the latter two 0.55 and 0.45; storing
+// a tile takes about 4.5, 2 and 1.5, an exchange between ranks 1.  Ranks only
+// where all tiles run at once.
+Cut choose_cut(bool symmetric, int rows, int cols, int batch, int k_blocks, bool fine, const Device &d)
+{
+    auto tiles = [&](int bm, int bn) {
+        return static_cast<long long>(tiles_of(symmetric, (rows + bm - 1) / bm, (cols + bn - 1) / bn)) * batch;
     };
-    const long long small = tiles(128);
+    auto rounds = [&](long long n) { return static_cast<double>((n + d.sms - 1) / d.sms); };
+    const long long small = tiles(128, 128);
     const double block = fine ? 0.45 : 0.34;
-    Cut best{false, 1};
-    double least = static_cast<double>((small + sms - 1) / sms) * k_blocks * block + 1.5;
-    for (int ranks = 2; ranks <= 8; ranks *= 2) {
-        // Clusters of eight leave SMs of a GPC over: 128 of 152 CTAs run.
-        if (small * ranks > sms * 5 / 6 || k_blocks < 2 * ranks)
-            break;
-        const double t = (k_blocks + ranks - 1) / ranks * block + 2.5;
+    Cut best{128, 128, 1};
+    double least = rounds(small) * k_blocks * block + 1.5;
+    auto offer = [&](const Cut &cut, double t) {
         if (t < least) {
             least = t;
-            best = Cut{false, ranks};
+            best = cut;
         }
-    }
+    };
+    for (int ranks = 2; ranks <= 8 && k_blocks >= 2 * ranks && small * ranks <= d.sms; ranks *= 2)
+        if (small <= cluster_room(ranks, d))
+            offer(Cut{128, 128, ranks}, (k_blocks + ranks - 1) / ranks * block + 2.5);
+    if (!symmetric)
+        offer(Cut{128, 192, 1}, rounds(tiles(128, 192)) * k_blocks * (fine ? 0.55 : 0.43) + 2.0);
     if (!fine) {
-        const long long rounds = (tiles(256) + sms - 1) / sms;
-        if (static_cast<double>(rounds) * (k_blocks * 0.65 + 4.5) < least)
-            best = Cut{true, 1};
+        const double n = rounds(tiles(256, 256));
+        offer(Cut{256, 256, 1}, n * (k_blocks * 0.65 + 4.5));
     }
     return best;
 }
@@ -986,8 +1021,11 @@ template <bool RightMN>
 int launch_product(const Cut &cut, const Maps &maps, Product p, const Device &d, cudaStream_t s)
 {
     p.ranks = cut.ranks;
-    if (cut.large)
+    if (cut.rows == 256)
         return launch_product_t<2, 256, 3, RightMN, false>(maps, p, d, s);
+    if constexpr (RightMN)
+        if (cut.cols == 192)
+            return launch_product_t<1, 192, 4, RightMN, false>(maps, p, d, s);
     return cut.ranks > 1 ? launch_product_t<1, 128, 4, RightMN, true>(maps, p, d, s)
                          : launch_product_t<1, 128, 4, RightMN, false>(maps, p, d, s);
 }
@@ -1006,11 +1044,9 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
     // The cuts of X X^T, of the square and of Q X, for the K blocks of the
     // passes a middle step makes.
     const int kr = (l.r + BK - 1) / BK, kc = (l.c + BK - 1) / BK;
-    const Cut cut_a = choose_cut(true, l.r, l.r, nb, (wide_result ? 3 : 1) * kc, wide_result, d.sms);
-    const Cut cut_s = choose_cut(true, l.r, l.r, nb, (wide_result ? 3 : 1) * kr + std::min(kr, 4), wide_result, d.sms);
-    const Cut cut_x = choose_cut(false, l.r, l.c, nb, (wide_result ? 5 : 2) * kr + std::min(kr, 2), wide_result, d.sms);
-    const uint32_t side_a = cut_a.large ? 256 : 128, side_s = cut_s.large ? 256 : 128,
-                   side_x = cut_x.large ? 256 : 128;
+    const Cut cut_a = choose_cut(true, l.r, l.r, nb, (wide_result ? 3 : 1) * kc, wide_result, d);
+    const Cut cut_s = choose_cut(true, l.r, l.r, nb, (wide_result ? 3 : 1) * kr + std::min(kr, 4), wide_result, d);
+    const Cut cut_x = choose_cut(false, l.r, l.c, nb, (wide_result ? 5 : 2) * kr + std::min(kr, 2), wide_result, d);
     CUtensorMap x_load[2], x_columns[2], a_load, a_diag_load, q_load, q_diag_load;
     CUtensorMap to_x[2], to_a[4], to_q[4], to_out; // a and q: store, mirror, store_diag, mirror_diag
     int st = GEMM_OK;
@@ -1019,15 +1055,15 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
             st = encode(map, m, cols, rows, swizzle);
     };
     for (int i = 0; i < 2; ++i) {
-        enc(&x_load[i], x[i], BK, side_a, 128);
+        enc(&x_load[i], x[i], BK, cut_a.rows, 128);
         if (st == GEMM_OK)
-            st = encode_column_groups(&x_columns[i], x[i], side_x);
+            st = encode_column_groups(&x_columns[i], x[i], cut_x.cols);
         enc(&to_x[i], x[i], 64, 32, 128);
     }
-    enc(&a_load, a, BK, side_s, 128);
-    enc(&a_diag_load, a_diag, BK, side_s, 128);
-    enc(&q_load, q, BK, side_x, 128);
-    enc(&q_diag_load, q_diag, BK, side_x, 128);
+    enc(&a_load, a, BK, cut_s.rows, 128);
+    enc(&a_diag_load, a_diag, BK, cut_s.rows, 128);
+    enc(&q_load, q, BK, cut_x.rows, 128);
+    enc(&q_diag_load, q_diag, BK, cut_x.rows, 128);
     auto stores = [&](CUtensorMap *to, const Planes &m, const Planes &m_diag) {
         enc(&to[0], m, 64, 32, 128);
         enc(&to[1], m, 32, 64, 64);

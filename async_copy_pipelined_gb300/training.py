@@ -12,6 +12,7 @@ current stream) without synchronising.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import async_copy_pipelined_gb300 as _pg
 
@@ -37,15 +38,16 @@ def bind(l):
     return l
 
 
-_torch = None
+_torch = _short = None
 _CODES = {}
 
 
 def _load():
     """torch, on the first call: importing this package does not import it."""
-    global _torch
+    global _torch, _short
     if _torch is None:
         import torch
+        _short = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _CODES[torch.float32] = F32
         _CODES[torch.bfloat16] = BF16
         _torch = torch
@@ -55,8 +57,7 @@ def _load():
 def _raw_stream(index):
     """The current stream's handle (torch's own short cut to it where it has
     one: building a Stream object takes longer than the launch)."""
-    short = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
-    return short(index) if short is not None else _torch.cuda.current_stream(index).cuda_stream
+    return _short(index) if _short is not None else _torch.cuda.current_stream(index).cuda_stream
 
 
 def _dtype(t, name):
@@ -64,6 +65,11 @@ def _dtype(t, name):
     if code is None:
         raise TypeError(f"{name} must be float32 or bfloat16, not {t.dtype}")
     return code
+
+
+def _lib():
+    """The loaded library (without the lock once it is there)."""
+    return _pg._lib or _pg.lib()
 
 
 def _rows(t, name):
@@ -101,7 +107,7 @@ def _vector(t, name, n, device):
         return None
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, x on {device}: all operands must be on one device")
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be {n} contiguous elements")
     return t.data_ptr()
 
@@ -173,6 +179,33 @@ def _workspace(kind, device, handle, nbytes, other):
     return buf
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_bytes(device, rows, cols):
+    """Workspace of layer_norm_backward for these sizes (a pure function of
+    them and the device)."""
+    need = ctypes.c_size_t()
+    _call(device, "layer_norm_backward_workspace", _lib().layer_norm_backward_workspace, rows, cols,
+          ctypes.byref(need))
+    return need.value
+
+
+@functools.lru_cache(maxsize=256)
+def _orthogonalize_bytes(device, batch, m, n, dtype):
+    need = ctypes.c_size_t()
+    _call(device, "orthogonalize_workspace", _lib().orthogonalize_workspace, batch, m, n, dtype, ctypes.byref(need))
+    return need.value
+
+
+@functools.lru_cache(maxsize=64)
+def _triples(coefficients, steps):
+    """coefficients as the library takes them: 3 * steps floats."""
+    per_step = coefficients if hasattr(coefficients[0], "__len__") else (coefficients,) * steps
+    flat = [float(v) for c in per_step for v in c]
+    if len(flat) != 3 * steps or steps < 1:
+        raise ValueError("coefficients must be one (a, b, c), or one for each of one or more steps")
+    return (ctypes.c_float * len(flat))(*flat)
+
+
 def layer_norm(x, weight=None, bias=None, out=None, *, eps=1e-5, stats=False, stream=None):
     """Layer norm over the last dimension of x (float32 or bfloat16).
 
@@ -186,10 +219,10 @@ def layer_norm(x, weight=None, bias=None, out=None, *, eps=1e-5, stats=False, st
     layer_norm_backward takes; otherwise y alone."""
     torch = _load()
     dt = _dtype(x, "x")
-    rows = _rows(x, "x")
+    rows, cols, ldx = _rows(x, "x")
     device = x.device
     handle, other = _enter(device, stream)
-    pw, pb = _vector(weight, "weight", rows[1], device), _vector(bias, "bias", rows[1], device)
+    pw, pb = _vector(weight, "weight", cols, device), _vector(bias, "bias", cols, device)
     wdt = F32
     if weight is not None:
         wdt = _dtype(weight, "weight")
@@ -198,23 +231,24 @@ def layer_norm(x, weight=None, bias=None, out=None, *, eps=1e-5, stats=False, st
     elif bias is not None:
         wdt = _dtype(bias, "bias")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=device)
-        ldy = rows[1]
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        ldy = cols
     else:
         if out.device != device:
             raise ValueError(f"out is on {out.device}, x on {device}: all operands must be on one device")
         if out.shape != x.shape or out.dtype != x.dtype:
             raise ValueError("out must have x's shape and type")
         out_rows = _rows(out, "out")
-        _refuse_overlap(out, out_rows, x, rows, "x", "out")
+        _refuse_overlap(out, out_rows, x, (rows, cols, ldx), "x", "out")
         ldy = out_rows[2]
     mean = rstd = pm = pr = None
     if stats:
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
+        shape = x.shape[:-1]
+        mean = torch.empty(shape, dtype=torch.float32, device=device)
+        rstd = torch.empty(shape, dtype=torch.float32, device=device)
         pm, pr = mean.data_ptr(), rstd.data_ptr()
-    _call(device, "layer_norm", _pg.lib().layer_norm, rows[0], rows[1], x.data_ptr(), rows[2], dt, pw, pb, wdt,
-          out.data_ptr(), ldy, pm, pr, eps, handle)
+    _call(device, "layer_norm", _lib().layer_norm, rows, cols, x.data_ptr(), ldx, dt, pw, pb, wdt, out.data_ptr(), ldy,
+          pm, pr, eps, handle)
     if other is not None:
         _record(other, x, weight, bias, out, mean, rstd)
     return (out, mean, rstd) if stats else out
@@ -245,7 +279,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, *, stream=None
             raise ValueError(f"{name} must be {rows[0]} contiguous float32 values")
     pw = _vector(weight, "weight", rows[1], device)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
         lddx = rows[1]
     else:
         if out.device != device:
@@ -256,17 +290,14 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, *, stream=None
         _refuse_overlap(out, out_rows, x, rows, "x", "out")
         _refuse_overlap(out, out_rows, dy, dy_rows, "dy", "out")
         lddx = out_rows[2]
-    l = _pg.lib()
+    l = _lib()
     wdt, ws_bytes = F32, 0
     dweight = dbias = ws = pdw = pdb = pws = None
     if weight is not None:
         wdt = _dtype(weight, "weight")
-        dweight = torch.empty(rows[1], dtype=weight.dtype, device=device)
-        dbias = torch.empty(rows[1], dtype=weight.dtype, device=device)
-        need = ctypes.c_size_t()
-        _call(device, "layer_norm_backward_workspace", l.layer_norm_backward_workspace, rows[0], rows[1],
-              ctypes.byref(need))
-        ws = _workspace("layer_norm_backward", device, handle, need.value, other)
+        dweight = torch.empty_like(weight)
+        dbias = torch.empty_like(weight)
+        ws = _workspace("layer_norm_backward", device, handle, _norm_bytes(device, rows[0], rows[1]), other)
         ws_bytes = ws.numel()
         pdw, pdb, pws = dweight.data_ptr(), dbias.data_ptr(), ws.data_ptr()
     _call(device, "layer_norm_backward", l.layer_norm_backward, rows[0], rows[1], dy.data_ptr(), dy_rows[2],
@@ -332,23 +363,19 @@ def orthogonalize(G, out=None, *, steps=5, coefficients=COEFFICIENTS, eps=1e-7, 
     _, _, _, ldo, o_batch = _matrices(out, "out")
     if batch > 1 and out.numel() and o_batch < ldo * (m - 1) + n:
         raise ValueError("the matrices of out overlap in memory")
-    triples = [float(v) for c in (coefficients if hasattr(coefficients[0], "__len__") else [coefficients] * steps)
-               for v in c]
-    if len(triples) != 3 * steps or steps < 1:
-        raise ValueError("coefficients must be one (a, b, c), or one for each of one or more steps")
-    l = _pg.lib()
-    need = ctypes.c_size_t()
-    _call(device, "orthogonalize_workspace", l.orthogonalize_workspace, batch, m, n, odt, ctypes.byref(need))
+    triples = _triples(tuple(tuple(c) if hasattr(c, "__len__") else c for c in coefficients), steps)
+    l = _lib()
+    need = _orthogonalize_bytes(device, batch, m, n, odt)
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError('workspace must be "auto" or a uint8 CUDA tensor')
-        ws = _workspace("orthogonalize", device, handle, need.value, other)
+        ws = _workspace("orthogonalize", device, handle, need, other)
     else:
         ws = workspace
         if ws.device != device:
             raise ValueError(f"workspace is on {ws.device}, G on {device}")
     _call(device, "orthogonalize", l.orthogonalize, batch, m, n, G.data_ptr(), ldg, g_batch, dt, out.data_ptr(), ldo,
-          o_batch, odt, steps, (ctypes.c_float * len(triples))(*triples), eps, ws.data_ptr(),
+          o_batch, odt, steps, triples, eps, ws.data_ptr(),
           ws.numel() * ws.element_size(), handle)
     if other is not None:
         _record(other, G, out, ws)
