@@ -164,6 +164,8 @@ __global__ void __launch_bounds__(32 * kFinishRows) finish_kernel(const Backward
     }
 }
 
+constexpr long long kAloneElements = 32768;
+
 // Most partial sums of a column that any variant makes.
 int backward_parts(int rows, int sms)
 {
@@ -173,28 +175,28 @@ int backward_parts(int rows, int sms)
 
 // Elements per thread `e`, rows at a time, and where they come from.  The
 // ring pays once a group has several rows to run ahead over; below that the
-// threads load their own.  `full`: there is a variant for rows without a rest.
+// threads load their own.  `ctas`: how many share the rows.  `full`: there is a variant for rows without a rest.
 Plan spread(int rows, int cols, int e, int max_threads, int streams, int parameters, bool vectors, bool full,
-            size_t size, const Device &d)
+            size_t size, const Device &d, int ctas)
 {
     Plan plan = {};
     const int tpr = (cols + e * 32 - 1) / (e * 32) * 32;
     if (tpr > max_threads)
         return plan;
     plan.elements = e;
-    const int groups = std::max(1, std::min(max_threads / tpr, (rows + d.sms - 1) / d.sms));
+    const int groups = std::max(1, std::min(max_threads / tpr, (rows + ctas - 1) / ctas));
     const int trips = (rows + groups - 1) / groups;
     const int row_bytes = cols * static_cast<int>(size);
     const int slot_bytes = vectors ? row_bytes : (row_bytes + 15 + 15) / 16 * 16;
     const int fixed = parameters * parameter_floats(cols) * 4;
     const int layer = groups * streams * slot_bytes; // one slot of every group
     const int slots = std::min({kMaxSlots, std::max(2, kRingBytes / layer), (kSmemBytes - fixed) / layer});
-    const bool ring = trips > 2 * d.sms && slots >= 2;
+    const bool ring = trips > 2 * ctas && slots >= 2;
     plan.source = !ring ? (vectors ? kVector : kScalar)
                   : !vectors ? kRingScalar
                   : cols == tpr * e && full ? kRingFull : kRingVector;
     plan.shape = Shape{tpr, groups, slots, slot_bytes, d.status, call_wait_limit_ns(), call_withhold()};
-    plan.grid = std::min(trips, d.sms);
+    plan.grid = std::min(trips, ctas);
     plan.smem = ring ? fixed + slots * groups * streams * slot_bytes : 0;
     return plan;
 }
@@ -216,7 +218,7 @@ int launch_forward(const Forward &p, const Device &d, cudaStream_t s)
     // 16 elements a thread give a single row the most threads; 32 give many
     // rows the most groups, whose reductions overlap.
     const int e = p.cols <= 512 || ((p.rows <= 2 * d.sms || !vectors) && p.cols <= 8192) ? 16 : 32;
-    Plan plan = spread(p.rows, p.cols, e, forward_threads(e), 1, 2, vectors, true, sizeof(T), d);
+    Plan plan = spread(p.rows, p.cols, e, forward_threads(e), 1, 2, vectors, true, sizeof(T), d, d.sms);
     if (plan.elements != 0) {
         if (!from_ring(plan.source)) // no ring to keep the memory system busy: every CTA that fits
             plan.grid = std::min((p.rows + plan.shape.groups - 1) / plan.shape.groups, 4 * d.sms);
@@ -251,7 +253,13 @@ int launch_backward(Backward p, const Device &d, cudaStream_t s)
                          vector_parameter(p.weight);
     // 16 elements leave room for the two column sums of each in registers.
     const int e = p.cols <= 8192 ? 16 : 32;
-    Plan plan = spread(p.rows, p.cols, e, kBackwardThreads, 2, 1, vectors, e == 16, sizeof(T), d);
+    // A gradient of few elements goes to one CTA, which needs no second kernel
+    // to add up column sums: 32 x 1024 bfloat16 rows take it 7 us and two
+    // kernels 5 + 3, of which the second launch costs the host more.
+    // Not where its groups would take many rows in turn (500 x 64: 39 us).
+    const int at_once = std::max(1, kBackwardThreads / ((p.cols + 16 * 32 - 1) / (16 * 32) * 32));
+    const bool alone = static_cast<long long>(p.rows) * p.cols <= kAloneElements && p.rows <= 8 * at_once;
+    Plan plan = spread(p.rows, p.cols, e, kBackwardThreads, 2, 1, vectors, e == 16, sizeof(T), d, alone ? 1 : d.sms);
     if (plan.elements != 0 && p.rows > 0) {
         p.parts = plan.grid;
         const int st = launch_backward_rows(p, kBf16, plan, d, s);

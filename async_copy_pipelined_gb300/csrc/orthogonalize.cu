@@ -91,6 +91,12 @@ struct Maps {
 
 // D (rows x cols, a batch of them) = sum over the passes of left plane times
 // right plane over k, scaled by alpha, plus diag on the diagonal.
+// Short sums show what the four additions of a K block lose: with a side r of
+// up to this every MMA has an accumulator of its own.
+constexpr int kStepSide = 128;
+
+enum Fine { kWhole, kPerBlock, kPerStep }; // one for all, one per K block, one per MMA
+
 struct Product {
     int rows, cols, k, batch;
     int symmetric; // compute the tiles on and above the diagonal, store both
@@ -98,7 +104,7 @@ struct Product {
     int passes;
     Pass pass[kMaxPasses];
     int ranks; // CTAs that share a tile's K blocks
-    int fine; // an accumulator for each K block of the last pass, one for the passes before it
+    int fine; // Fine: accumulators of the last pass; the passes before it have one
     float alpha, diag;
     int alpha_power, diag_power; // of f
     const float *f;              // one per matrix
@@ -195,11 +201,13 @@ __device__ __forceinline__ void pass_range(const Pass &pass, int k, int row0, in
 struct Blocks {
     int before, all;
     int lo, hi; // this CTA's
-    // Whether an accumulator ends with block kb, and how many there are.
-    __device__ __forceinline__ bool ends(int kb, bool fine) const { return kb == hi - 1 || (fine && kb >= before - 1); }
-    __device__ __forceinline__ int accumulators(bool fine) const
+    // How many accumulators that takes.
+    __device__ __forceinline__ int accumulators(int fine) const
     {
-        return fine ? (lo < min(before, hi) ? 1 : 0) + max(0, hi - max(lo, before)) : (lo < hi ? 1 : 0);
+        if (fine == kWhole)
+            return lo < hi ? 1 : 0;
+        return (lo < min(before, hi) ? 1 : 0) +
+               max(0, hi - max(lo, before)) * (fine == kPerStep ? BK / kUmmaK : 1);
     }
 };
 
@@ -299,7 +307,7 @@ struct Staging {
 
 // RightMN: the right operand's rows are k (Q X); otherwise its rows are D's
 // columns (X X^T, and the symmetric A A).
-template <int MH, int BN, int S, bool RightMN, bool Split>
+template <int MH, int BN, int S, bool RightMN, bool Split, bool Steps = false>
 __global__ void __launch_bounds__(Tile<MH, BN, S, Split>::kThreads, 1)
     product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Product p)
 {
@@ -418,61 +426,96 @@ __global__ void __launch_bounds__(Tile<MH, BN, S, Split>::kThreads, 1)
             cluster_sync(); // the epilogue's exchange
     } else if (warp == 1) {
         // ------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            int f = 0;
+        // (Steps, the path of Fine::kPerStep, is a kernel of its own: merely
+        // present in this loop it made 2048 x 2048 bfloat16 take 460 us
+        // instead of 407.)
+        // One thread's instructions stand between the MMAs: with descriptors
+        // built anew for each MMA the 256 x 256 tile took 0.65 us a K block,
+        // in which its MMAs take 0.52 at 1.96 GHz.  So they are built once;
+        // stages and K steps add to their address field (16-byte units).
+        {
+            const uint32_t on = lane == 0 ? 1u : 0u;
+            constexpr uint64_t kStageStep = T::kStageBytes >> 4, kRowsStep = (kUmmaM * 128) >> 4;
+            // K step: 32 bytes along a K-major row; 16 rows of 128 bytes of an
+            // MN-major box.
+            constexpr uint64_t kLeftStep = (kUmmaK * 2) >> 4, kRightStep = (RightMN ? kUmmaK * 128 : kUmmaK * 2) >> 4;
+            const uint64_t left0 = smem_desc_sw128(base, 16, 1024);
+            const uint64_t right0 = smem_desc_sw128(base + T::kLeftBytes, RightMN ? kAtomBytes : 16, 1024);
+            uint64_t left = left0, right = right0;
+            uint32_t stage = 0, phase = 0;
             bool ok = true;
             int acc = 0; // accumulators begun
+            uint32_t d_tmem = tmem_base, full_bar = tmem_full0;
+            auto begin = [&]() { // an accumulator
+                const int slot = acc % T::kAccBufs;
+                const uint32_t use_parity = static_cast<uint32_t>((acc / T::kAccBufs) & 1);
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(tmem_empty0 + 8u * slot, use_parity ^ 1u, p.wait_limit_ns))) {
+                    if (on)
+                        record_error(p.status, kErrFamilyOrthogonalize | kErrRoleMma);
+                    return false;
+                }
+                tc_fence_after_sync();
+                d_tmem = tmem_base + static_cast<uint32_t>(slot * MH * BN);
+                full_bar = tmem_full0 + 8u * slot;
+                ++acc;
+                return true;
+            };
             for (int t = first_tile; t < num_tiles && ok; t += tile_step) {
                 const TileAt at = tile_at(t, symmetric, tiles_m, tiles_n);
                 const Blocks blocks = tile_blocks<BM, BN>(p, at, rank);
-                uint32_t d_tmem = tmem_base, full_bar = tmem_full0;
-                bool fresh = true; // the next block begins an accumulator
-                for (int kb = blocks.lo; kb < blocks.hi; ++kb, ++f) {
-                    if (fresh) {
-                        const int slot = acc % T::kAccBufs;
-                        const uint32_t use_parity = static_cast<uint32_t>((acc / T::kAccBufs) & 1);
-                        if (!mbar_wait_bounded(tmem_empty0 + 8u * slot, use_parity ^ 1u, p.wait_limit_ns)) {
-                            record_error(p.status, kErrFamilyOrthogonalize | kErrRoleMma);
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after_sync();
-                        d_tmem = tmem_base + static_cast<uint32_t>(slot * MH * BN);
-                        full_bar = tmem_full0 + 8u * slot;
-                        ++acc;
+                bool fresh = true; // the next MMA begins an accumulator
+                for (int kb = blocks.lo; kb < blocks.hi; ++kb) {
+                    const bool steps = Steps && kb >= blocks.before;
+                    if (fresh && !steps && !begin()) {
+                        ok = false;
+                        break;
                     }
-                    if (!ring.consumer_wait(f, p.wait_limit_ns)) {
-                        record_error(p.status, kErrFamilyOrthogonalize | kErrRoleMma);
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(ring.full0 + 8u * stage, phase, p.wait_limit_ns))) {
+                        if (on)
+                            record_error(p.status, kErrFamilyOrthogonalize | kErrRoleMma);
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
-                    const uint32_t a_addr = base + static_cast<uint32_t>(f % S) * T::kStageBytes;
-                    const uint32_t b_addr = a_addr + T::kLeftBytes;
-#pragma unroll
-                    for (int ks = 0; ks < BK / kUmmaK; ++ks) {
-                        // K step: 32 bytes along a K-major row; 16 rows of 128
-                        // bytes of an MN-major box.
-                        const uint64_t bdesc =
-                            RightMN ? smem_desc_sw128(b_addr + ks * kUmmaK * 128, kAtomBytes, 1024)
-                                    : smem_desc_sw128(b_addr + ks * kUmmaK * 2, 16, 1024);
-#pragma unroll
-                        for (int h = 0; h < MH; ++h) {
-                            const uint64_t adesc =
-                                smem_desc_sw128(a_addr + h * (kUmmaM * 128) + ks * kUmmaK * 2, 16, 1024);
-                            mma_f16_ss(d_tmem + static_cast<uint32_t>(h * BN), adesc, bdesc, kIdesc,
-                                       (!fresh || ks != 0) ? 1u : 0u);
+                    bool stepped = false;
+                    if constexpr (Steps) {
+                        stepped = steps;
+                        for (int ks = 0; ks < BK / kUmmaK && ok && steps; ++ks) {
+                            ok = begin();
+                            if (ok) {
+                                mma_f16_ss_if(on, d_tmem, left + ks * kLeftStep, right + ks * kRightStep, kIdesc, 0u);
+                                mma_commit_if(on, full_bar);
+                            }
                         }
                     }
-                    mma_commit(ring.empty_bar(f)); // stage free once these MMAs have read it
-                    fresh = blocks.ends(kb, p.fine != 0);
-                    if (fresh)
-                        mma_commit(full_bar); // accumulator complete
+                    if (!stepped) {
+#pragma unroll
+                        for (int ks = 0; ks < BK / kUmmaK; ++ks)
+#pragma unroll
+                            for (int h = 0; h < MH; ++h)
+                                mma_f16_ss_if(on, d_tmem + static_cast<uint32_t>(h * BN),
+                                           left + (ks * kLeftStep + h * kRowsStep), right + ks * kRightStep, kIdesc,
+                                           ks == 0 && fresh ? 0u : 1u);
+                        fresh = kb == blocks.hi - 1 || (MH == 1 && p.fine != kWhole && kb >= blocks.before - 1);
+                        if (fresh)
+                            mma_commit_if(on, full_bar); // accumulator complete
+                    }
+                    if (!ok)
+                        break;
+                    mma_commit_if(on, ring.empty0 + 8u * stage); // stage free once these MMAs have read it
+                    left += kStageStep;
+                    right += kStageStep;
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                        left = left0;
+                        right = right0;
+                    }
                 }
             }
             // Every MMA this thread issued must finish before tensor memory is freed.
-            mma_commit(mma_done);
-            if (!mbar_wait_bounded(mma_done, 0, p.wait_limit_ns))
+            mma_commit_if(on, mma_done);
+            if (!mbar_wait_bounded(mma_done, 0, p.wait_limit_ns) && on)
                 record_error(p.status, kErrFamilyOrthogonalize | kErrRoleDrain);
         }
         if constexpr (Split)
@@ -647,7 +690,7 @@ __global__ void __launch_bounds__(Tile<MH, BN, S, Split>::kThreads, 1)
             };
 
             if constexpr (T::kEpiCols == 64) {
-                const int parts = tile_blocks<BM, BN>(p, at, rank).accumulators(p.fine != 0);
+                const int parts = tile_blocks<BM, BN>(p, at, rank).accumulators(p.fine);
                 unsigned long long v[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
@@ -930,12 +973,12 @@ int encode_column_groups(CUtensorMap *map, const Planes &m, uint32_t columns)
     return encode_tensor_map(map, kElement16, m.base, 4, dims, pitches, box, 128);
 }
 
-template <int MH, int BN, int S, bool RightMN, bool Split>
+template <int MH, int BN, int S, bool RightMN, bool Split, bool Steps = false>
 int launch_product_t(const Maps &maps, const Product &p, const Device &d, cudaStream_t s)
 {
     using T = Tile<MH, BN, S, Split>;
     static std::atomic<unsigned long long> limit_set[kMaxDevices];
-    auto *kernel = product_kernel<MH, BN, S, RightMN, Split>;
+    auto *kernel = product_kernel<MH, BN, S, RightMN, Split, Steps>;
     if (ensure_smem_limit(kernel, T::kSmem, d.index, d.ctx, limit_set) != GEMM_OK)
         return GEMM_ERR_CUDA;
     const long long tiles = static_cast<long long>(tiles_of(p.symmetric != 0, (p.rows + T::BM - 1) / T::BM,
@@ -989,14 +1032,14 @@ int cluster_room(int ranks, const Device &d)
 // in), with an accumulator of its own the latter two 0.55 and 0.45; storing
 // a tile takes about 4.5, 2 and 1.5, an exchange between ranks 1.  Ranks only
 // where all tiles run at once.
-Cut choose_cut(bool symmetric, int rows, int cols, int batch, int k_blocks, bool fine, const Device &d)
+Cut choose_cut(bool symmetric, int rows, int cols, int batch, int k_blocks, int fine, const Device &d)
 {
     auto tiles = [&](int bm, int bn) {
         return static_cast<long long>(tiles_of(symmetric, (rows + bm - 1) / bm, (cols + bn - 1) / bn)) * batch;
     };
     auto rounds = [&](long long n) { return static_cast<double>((n + d.sms - 1) / d.sms); };
     const long long small = tiles(128, 128);
-    const double block = fine ? 0.45 : 0.34;
+    const double block = fine != kWhole ? 0.45 : 0.34;
     Cut best{128, 128, 1};
     double least = rounds(small) * k_blocks * block + 1.5;
     auto offer = [&](const Cut &cut, double t) {
@@ -1008,26 +1051,31 @@ Cut choose_cut(bool symmetric, int rows, int cols, int batch, int k_blocks, bool
     for (int ranks = 2; ranks <= 8 && k_blocks >= 2 * ranks && small * ranks <= d.sms; ranks *= 2)
         if (small <= cluster_room(ranks, d))
             offer(Cut{128, 128, ranks}, (k_blocks + ranks - 1) / ranks * block + 2.5);
-    if (!symmetric)
-        offer(Cut{128, 192, 1}, rounds(tiles(128, 192)) * k_blocks * (fine ? 0.55 : 0.43) + 2.0);
-    if (!fine) {
+    if (!symmetric && fine != kPerStep)
+        offer(Cut{128, 192, 1}, rounds(tiles(128, 192)) * k_blocks * (fine != kWhole ? 0.55 : 0.43) + 2.0);
+    if (fine == kWhole) {
         const double n = rounds(tiles(256, 256));
         offer(Cut{256, 256, 1}, n * (k_blocks * 0.65 + 4.5));
     }
     return best;
 }
 
+constexpr int kSmallTileStages = 6;
+
 template <bool RightMN>
 int launch_product(const Cut &cut, const Maps &maps, Product p, const Device &d, cudaStream_t s)
 {
     p.ranks = cut.ranks;
+    if (p.fine == kPerStep) // 128 x 128 tiles (choose_cut)
+        return cut.ranks > 1 ? launch_product_t<1, 128, 4, RightMN, true, true>(maps, p, d, s)
+                             : launch_product_t<1, 128, kSmallTileStages, RightMN, false, true>(maps, p, d, s);
     if (cut.rows == 256)
         return launch_product_t<2, 256, 3, RightMN, false>(maps, p, d, s);
     if constexpr (RightMN)
         if (cut.cols == 192)
             return launch_product_t<1, 192, 4, RightMN, false>(maps, p, d, s);
     return cut.ranks > 1 ? launch_product_t<1, 128, 4, RightMN, true>(maps, p, d, s)
-                         : launch_product_t<1, 128, 4, RightMN, false>(maps, p, d, s);
+                         : launch_product_t<1, 128, kSmallTileStages, RightMN, false>(maps, p, d, s);
 }
 
 int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigned int *status, cudaStream_t s)
@@ -1043,10 +1091,11 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
 
     // The cuts of X X^T, of the square and of Q X, for the K blocks of the
     // passes a middle step makes.
+    const int fine = !wide_result ? kWhole : l.r <= kStepSide ? kPerStep : kPerBlock;
     const int kr = (l.r + BK - 1) / BK, kc = (l.c + BK - 1) / BK;
-    const Cut cut_a = choose_cut(true, l.r, l.r, nb, (wide_result ? 3 : 1) * kc, wide_result, d);
-    const Cut cut_s = choose_cut(true, l.r, l.r, nb, (wide_result ? 3 : 1) * kr + std::min(kr, 4), wide_result, d);
-    const Cut cut_x = choose_cut(false, l.r, l.c, nb, (wide_result ? 5 : 2) * kr + std::min(kr, 2), wide_result, d);
+    const Cut cut_a = choose_cut(true, l.r, l.r, nb, (wide_result ? 3 : 1) * kc, fine, d);
+    const Cut cut_s = choose_cut(true, l.r, l.r, nb, (wide_result ? 3 : 1) * kr + std::min(kr, 4), fine, d);
+    const Cut cut_x = choose_cut(false, l.r, l.c, nb, (wide_result ? 5 : 2) * kr + std::min(kr, 2), fine, d);
     CUtensorMap x_load[2], x_columns[2], a_load, a_diag_load, q_load, q_diag_load;
     CUtensorMap to_x[2], to_a[4], to_q[4], to_out; // a and q: store, mirror, store_diag, mirror_diag
     int st = GEMM_OK;
@@ -1117,7 +1166,7 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
     base.status = status;
     base.wait_limit_ns = call_wait_limit_ns();
     base.withhold = call_withhold();
-    base.fine = wide_result;
+    base.fine = fine;
     for (int step = 0; step < call.steps; ++step) {
         const float ca = call.coefficients[3 * step], cb = call.coefficients[3 * step + 1],
                     cc = call.coefficients[3 * step + 2];

@@ -278,25 +278,29 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
             v[j] = fma2(v[j], a, pair(2 * j == at ? diag : 0.0f, 2 * j + 1 == at ? diag : 0.0f));
     };
     const int k_blocks = p.r > 64 ? 2 : 1; // of A and Q
-    auto square_pass = [&](uint32_t left, uint32_t right, bool first) {
-        for (int kb = 0; kb < k_blocks; ++kb)
-            for (int ks = 0; ks < 4; ++ks) {
-                const uint32_t at = static_cast<uint32_t>(kb) * kColumnBlock + static_cast<uint32_t>(ks) * 32u;
-                mma_f16_ss(tmem, smem_desc_sw128(base + left + at, 16, 1024),
-                           smem_desc_sw128(base + right + at, 16, 1024), instruction(128, false),
-                           !first || kb != 0 || ks != 0 ? 1u : 0u);
-            }
+    // Descriptors of the first block; others add to the address field
+    // (16-byte units).  K-major: a K step is 32 bytes, a K block 16 KiB; the
+    // MN-major right operand of Q X: 16 rows and 64 rows of 128 bytes.
+    constexpr uint64_t kBlockStep = kColumnBlock >> 4, kStep = 32 >> 4, kRowStep = (16 * 128) >> 4;
+    const uint64_t k_major = smem_desc_sw128(base, 16, 1024), mn_major = smem_desc_sw128(base, kColumnBlock, 1024);
+    const uint32_t square_form = instruction(128, false), result_form = instruction(width, true);
+    auto square_pass = [&](uint32_t left, uint32_t right, int blocks, bool first) {
+        uint64_t l = k_major + (left >> 4), q = k_major + (right >> 4);
+        for (int kb = 0; kb < blocks; ++kb, l += kBlockStep, q += kBlockStep) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+                mma_f16_ss(tmem, l + ks * kStep, q + ks * kStep, square_form, !first || kb != 0 || ks != 0 ? 1u : 0u);
+        }
     };
     constexpr int kResult = 128; // accumulator of Q X, beside that of X X^T and the square
     auto result_pass = [&](uint32_t left, uint32_t right, bool first) {
-        for (int kb = 0; kb < k_blocks; ++kb)
+        uint64_t l = k_major + (left >> 4), q = mn_major + (right >> 4);
+        for (int kb = 0; kb < k_blocks; ++kb, l += kBlockStep, q += 4 * kRowStep) {
+#pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-                mma_f16_ss(tmem + kResult,
-                           smem_desc_sw128(base + left + static_cast<uint32_t>(kb) * kColumnBlock +
-                                               static_cast<uint32_t>(ks) * 32u, 16, 1024),
-                           smem_desc_sw128(base + right + static_cast<uint32_t>(kb * 64 + ks * 16) * 128u,
-                                           kColumnBlock, 1024),
-                           instruction(width, true), !first || kb != 0 || ks != 0 ? 1u : 0u);
+                mma_f16_ss(tmem + kResult, l + ks * kStep, q + ks * kRowStep, result_form,
+                           !first || kb != 0 || ks != 0 ? 1u : 0u);
+        }
     };
 
     for (int step = 0; step < p.steps; ++step) {
@@ -308,14 +312,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
         uint32_t w[32];
 
         // X X^T, over all ranks' columns.
-        multiply([&]() {
-            for (int kb = 0; kb < p.blocks; ++kb)
-                for (int ks = 0; ks < 4; ++ks) {
-                    const uint64_t d = smem_desc_sw128(
-                        base + kX0 + static_cast<uint32_t>(kb) * kColumnBlock + static_cast<uint32_t>(ks) * 32u, 16, 1024);
-                    mma_f16_ss(tmem, d, d, instruction(128, false), kb != 0 || ks != 0 ? 1u : 0u);
-                }
-        });
+        multiply([&]() { square_pass(kX0, kX0, p.blocks, true); });
         read(half * 64, v);
         const int unit = quarter * 2 + half, each = 8 / p.ranks, owner = unit / each;
         if (p.ranks > 1) {
@@ -371,9 +368,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
         if (cc != 0.0f) {
             // The square, in every rank, and Q in A's place.
             multiply([&]() {
-                square_pass(kA1, kA0, true);
-                square_pass(kA0, kA1, false);
-                square_pass(kA0, kA0, false);
+                square_pass(kA1, kA0, k_blocks, true);
+                square_pass(kA0, kA1, k_blocks, false);
+                square_pass(kA0, kA0, k_blocks, false);
             });
             read(half * 64, v);
             scale(v, kScaleQ * cc / (kScaleA * kScaleA) * fs,
