@@ -290,6 +290,8 @@ int enter(Device *d)
     return d->status ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
+constexpr int kMaxCols = 1 << 28; // a row's bytes and columns are counted in an int
+
 bool valid_dtype(int d) { return d == GEMM_DTYPE_F32 || d == GEMM_DTYPE_BF16; }
 
 bool aligned_to(const void *p, int dtype)
@@ -310,6 +312,8 @@ int layer_norm(int rows, int cols, const void *x, long long ldx, int dtype, cons
 {
     if (rows < 0 || cols < 1 || !ln::valid_dtype(dtype) || !ln::valid_dtype(weight_dtype))
         return GEMM_ERR_INVALID_ARG;
+    if (cols > ln::kMaxCols)
+        return GEMM_ERR_UNSUPPORTED;
     if (!(eps >= 0.0f) || !std::isfinite(eps) || (mean == nullptr) != (rstd == nullptr))
         return GEMM_ERR_INVALID_ARG;
     if (rows > 1 && (ldx < cols || ldy < cols))
@@ -335,6 +339,8 @@ int layer_norm_backward_workspace(int rows, int cols, size_t *bytes)
 {
     if (rows < 0 || cols < 1 || !bytes)
         return GEMM_ERR_INVALID_ARG;
+    if (cols > ln::kMaxCols)
+        return GEMM_ERR_UNSUPPORTED;
     *bytes = static_cast<size_t>(ln::backward_parts(rows, device_sms())) * 2u * static_cast<size_t>(cols) * 4u;
     return GEMM_OK;
 }
@@ -346,6 +352,8 @@ int layer_norm_backward(int rows, int cols, const void *dy, long long lddy, cons
 {
     if (rows < 0 || cols < 1 || !ln::valid_dtype(dtype) || !ln::valid_dtype(weight_dtype))
         return GEMM_ERR_INVALID_ARG;
+    if (cols > ln::kMaxCols)
+        return GEMM_ERR_UNSUPPORTED;
     if (rows > 1 && (ldx < cols || lddy < cols || lddx < cols))
         return GEMM_ERR_INVALID_ARG;
     if (rows > 0 && (!dy || !x || !dx || !mean || !rstd))

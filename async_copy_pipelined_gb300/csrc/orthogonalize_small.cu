@@ -240,11 +240,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
         fence_proxy_async_smem();
         tc_fence_before_sync();
         __syncthreads();
-        if (threadIdx.x == 0) {
+        if (warp == 0) { // one lane's instructions, the warp's addresses
             tc_fence_after_sync();
-            issue();
+            issue(lane == 0 ? 1u : 0u);
             if (product != p.withhold) // test hook: this product is never announced
-                mma_commit(done);
+                mma_commit_if(lane == 0 ? 1u : 0u, done);
         }
         ++product;
         __syncwarp();
@@ -284,22 +284,23 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     constexpr uint64_t kBlockStep = kColumnBlock >> 4, kStep = 32 >> 4, kRowStep = (16 * 128) >> 4;
     const uint64_t k_major = smem_desc_sw128(base, 16, 1024), mn_major = smem_desc_sw128(base, kColumnBlock, 1024);
     const uint32_t square_form = instruction(128, false), result_form = instruction(width, true);
-    auto square_pass = [&](uint32_t left, uint32_t right, int blocks, bool first) {
+    auto square_pass = [&](uint32_t on, uint32_t left, uint32_t right, int blocks, bool first) {
         uint64_t l = k_major + (left >> 4), q = k_major + (right >> 4);
         for (int kb = 0; kb < blocks; ++kb, l += kBlockStep, q += kBlockStep) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-                mma_f16_ss(tmem, l + ks * kStep, q + ks * kStep, square_form, !first || kb != 0 || ks != 0 ? 1u : 0u);
+                mma_f16_ss_if(on, tmem, l + ks * kStep, q + ks * kStep, square_form,
+                              !first || kb != 0 || ks != 0 ? 1u : 0u);
         }
     };
     constexpr int kResult = 128; // accumulator of Q X, beside that of X X^T and the square
-    auto result_pass = [&](uint32_t left, uint32_t right, bool first) {
+    auto result_pass = [&](uint32_t on, uint32_t left, uint32_t right, bool first) {
         uint64_t l = k_major + (left >> 4), q = mn_major + (right >> 4);
         for (int kb = 0; kb < k_blocks; ++kb, l += kBlockStep, q += 4 * kRowStep) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-                mma_f16_ss(tmem + kResult, l + ks * kStep, q + ks * kRowStep, result_form,
-                           !first || kb != 0 || ks != 0 ? 1u : 0u);
+                mma_f16_ss_if(on, tmem + kResult, l + ks * kStep, q + ks * kRowStep, result_form,
+                              !first || kb != 0 || ks != 0 ? 1u : 0u);
         }
     };
 
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
         uint32_t w[32];
 
         // X X^T, over all ranks' columns.
-        multiply([&]() { square_pass(kX0, kX0, p.blocks, true); });
+        multiply([&](uint32_t on) { square_pass(on, kX0, kX0, p.blocks, true); });
         read(half * 64, v);
         const int unit = quarter * 2 + half, each = 8 / p.ranks, owner = unit / each;
         if (p.ranks > 1) {
@@ -367,10 +368,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
 
         if (cc != 0.0f) {
             // The square, in every rank, and Q in A's place.
-            multiply([&]() {
-                square_pass(kA1, kA0, k_blocks, true);
-                square_pass(kA0, kA1, k_blocks, false);
-                square_pass(kA0, kA0, k_blocks, false);
+            multiply([&](uint32_t on) {
+                square_pass(on, kA1, kA0, k_blocks, true);
+                square_pass(on, kA0, kA1, k_blocks, false);
+                square_pass(on, kA0, kA0, k_blocks, false);
             });
             read(half * 64, v);
             scale(v, kScaleQ * cc / (kScaleA * kScaleA) * fs,
@@ -382,11 +383,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
         }
 
         // Q X: this rank's columns, in X's place or to the result.
-        multiply([&]() {
-            result_pass(kA1, kX0, true);
+        multiply([&](uint32_t on) {
+            result_pass(on, kA1, kX0, true);
             if (!last && !(first && exact))
-                result_pass(kA0, kX1, false);
-            result_pass(kA0, kX0, false);
+                result_pass(on, kA0, kX1, false);
+            result_pass(on, kA0, kX0, false);
         });
         for (int k = 0; k < 2; ++k) {
             const int block = half * 2 + k;

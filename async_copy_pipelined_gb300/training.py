@@ -329,6 +329,11 @@ def _matrices(t, name):
     return batch, m, n, pitch, t.stride(0) if batch > 1 else pitch * (m - 1) + n
 
 
+def _extent(t, m, n, batch, pitch, matrix_pitch):
+    first = t.data_ptr()
+    return first, first + ((batch - 1) * matrix_pitch + (m - 1) * pitch + n) * t.element_size()
+
+
 def orthogonalize(G, out=None, *, steps=5, coefficients=COEFFICIENTS, eps=1e-7, dtype=None, workspace="auto",
                   stream=None):
     """The orthogonalised form of a weight's update G, by Newton-Schulz products.
@@ -338,8 +343,8 @@ def orthogonalize(G, out=None, *, steps=5, coefficients=COEFFICIENTS, eps=1e-7, 
     float32 or bfloat16, rows at any pitch.  The result has G's shape and
     `dtype` (default: G's), which also sets the precision of the products: a
     bfloat16 result is within a small part of bfloat16's rounding of the
-    exact one, a float32 result near what float32 arithmetic gives, at about
-    three times the cost.
+    exact one, a float32 result what float32 arithmetic gives, at about four
+    times the cost.
 
     coefficients: one (a, b, c) for every step, or `steps` of them.  out:
     where the result goes (G itself for an in-place call).  workspace: "auto"
@@ -361,6 +366,10 @@ def orthogonalize(G, out=None, *, steps=5, coefficients=COEFFICIENTS, eps=1e-7, 
         raise ValueError("out must have G's shape and the type asked for")
     odt = _dtype(out, "out")
     _, _, _, ldo, o_batch = _matrices(out, "out")
+    if out.numel() and not (out.data_ptr() == G.data_ptr() and odt == dt and (ldo, o_batch) == (ldg, g_batch)):
+        a, b = _extent(out, m, n, batch, ldo, o_batch), _extent(G, m, n, batch, ldg, g_batch)
+        if a[0] < b[1] and b[0] < a[1]:
+            raise ValueError("out overlaps G in memory; it may only be G itself")
     if batch > 1 and out.numel() and o_batch < ldo * (m - 1) + n:
         raise ValueError("the matrices of out overlap in memory")
     triples = _triples(tuple(tuple(c) if hasattr(c, "__len__") else c for c in coefficients), steps)

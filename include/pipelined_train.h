@@ -38,7 +38,8 @@ enum gemm_dtype {
  * computed in float32 and rounded once to y's type.  The variance is taken
  * from differences to a mean, never as a difference of two large sums.
  *
- *   rows, cols   rows >= 0 (0: nothing is done), cols >= 1.
+ *   rows, cols   rows >= 0 (0: nothing is done), cols 1 .. 2^28 (beyond:
+ *                GEMM_ERR_UNSUPPORTED).
  *   x, ldx       rows x cols of `dtype`, ldx >= cols (any ldx when rows is 0
  *                or 1).  A pitch of any alignment works; rows whose base and
  *                pitch are 16-byte aligned move in 16-byte pieces.
@@ -113,14 +114,14 @@ int layer_norm_backward_workspace(int rows, int cols, size_t *bytes);
  *   batch, m, n   matrices and their sizes, each >= 0 (any of them 0: nothing
  *                 is done); sides to 2^20, m n below 2^31, batch to 65535.
  *   G             matrix b, element (i, j) at G[b*g_batch + i*ldg + j], of
- *                 `dtype`; ldg >= n, any alignment.  It is read whole before
- *                 anything is written to out.
+ *                 `dtype`; ldg >= n, any alignment.
  *   out           likewise with ldo, o_batch, of `out_dtype`; may be G
- *                 itself.  The products run in the precision this type asks
- *                 for: on GB300 the tensor cores' float16 pairs, with
- *                 float32 sums, whose error stays below bfloat16's rounding
- *                 for GEMM_DTYPE_BF16 and near float32 arithmetic's for
- *                 GEMM_DTYPE_F32 (at about three times the time).
+ *                 itself (pointer, pitches and type), otherwise shares no
+ *                 byte with it.  The products run in the precision this type
+ *                 asks for, on float16 planes with float32 sums: what they
+ *                 add to bfloat16's rounding stays below it for
+ *                 GEMM_DTYPE_BF16, and is that of float32 arithmetic for
+ *                 GEMM_DTYPE_F32 (at about four times the time).
  *   steps         1 .. 32.
  *   coefficients  3 * steps floats in host memory: a, b, c of each step.
  *                 c = 0 or |b| <= 8 |c|, and from singular values in [0, 1]

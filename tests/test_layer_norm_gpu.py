@@ -361,3 +361,64 @@ def test_refusals_on_device():
         pg.layer_norm(torch.empty((3, 0), device="cuda"))
     torch.cuda.synchronize()
     assert pg.device_status() == (0, 0)
+
+
+# Enough rows that every CTA's groups take several in turn: the rows come
+# through shared memory, whole vectors, rows without a rest, or element by
+# element where pitch or base is not 16-byte aligned.
+MANY = [
+    # rows, cols, dtype, weight dtype, pad, offset
+    (5200, 512, "bf16", "bf16", 0, 0), (9000, 264, "f32", "f32", 0, 0), (4000, 1024, "bf16", "f32", 0, 0),
+    (8000, 1000, "bf16", "bf16", 0, 0), (5000, 1001, "bf16", "f32", 0, 0), (5000, 999, "f32", "bf16", 0, 1),
+    (2600, 1024, "bf16", "bf16", 1, 3), (1300, 4096, "bf16", "f32", 0, 0), (1300, 4096, "f32", "f32", 8, 4),
+    (1300, 4100, "f32", "f32", 0, 0), (1500, 4097, "bf16", "bf16", 0, 0), (700, 8192, "bf16", "bf16", 0, 0),
+    (650, 8200, "bf16", "f32", 0, 0), (620, 8192, "f32", "f32", 0, 0), (640, 5003, "f32", "f32", 2, 1),
+    (320, 16384, "bf16", "bf16", 0, 0), (320, 12000, "bf16", "f32", 0, 0), (320, 12000, "f32", "f32", 0, 0),
+    (40000, 7, "bf16", "bf16", 0, 1), (20000, 33, "f32", "f32", 0, 0),
+]
+
+
+@pytest.mark.parametrize("rows,cols,dtype,wdtype,pad,offset", MANY)
+def test_many_rows_forward(rows, cols, dtype, wdtype, pad, offset):
+    test_forward(rows, cols, dtype, wdtype, pad, offset)
+
+
+@pytest.mark.parametrize("rows,cols,dtype,wdtype,pad,offset", MANY)
+def test_many_rows_backward(rows, cols, dtype, wdtype, pad, offset):
+    test_backward(rows, cols, dtype, wdtype, pad, offset)
+
+
+def test_neighbouring_rows_of_an_unaligned_matrix_stay_apart():
+    """Only whole 16-byte granules inside a row are copied ahead: what lies
+    between the rows, and before and behind them, is never part of one."""
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    rows, cols, pad = 4000, 1001, 3
+    x, x64, buf = _make(rows, cols, "bf16", pad, seed=1, offset=5)  # NaN in the gaps
+    y, mean, rstd = pg.layer_norm(x, eps=EPS, stats=True)
+    assert y.isfinite().all() and mean.isfinite().all()
+    dx, dw, db = pg.layer_norm_backward(x, x, mean, rstd, torch.ones(cols, device="cuda"))
+    assert dx.isfinite().all() and dw.isfinite().all() and db.isfinite().all()
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """A row the ring never fills: the kernels give up on it, say so, and the
+    next call is right."""
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    x = torch.randn((16000, 1024), device="cuda")
+    w = torch.ones(1024, device="cuda")
+    want, mean, rstd = pg.layer_norm(x, w, stats=True)
+    want_b = pg.layer_norm_backward(x, x, mean, rstd, w)
+    assert pg.device_status() == (0, 0)
+    for call in (lambda: pg.layer_norm(x, w), lambda: pg.layer_norm_backward(x, x, mean, rstd, w)):
+        try:
+            pg.testing_set_hooks(20_000_000, 3)  # 20 ms
+            call()
+        finally:
+            pg.testing_set_hooks()
+        status, detail = pg.device_status()
+        assert status == 6 and detail & 0xFF == 8
+    assert torch.equal(pg.layer_norm(x, w), want)
+    assert all(torch.equal(a, b) for a, b in zip(pg.layer_norm_backward(x, x, mean, rstd, w), want_b))
+    assert pg.device_status() == (0, 0)

@@ -344,3 +344,13 @@ def test_a_short_side_reports_a_wait_that_runs_out(m, n):
     assert status == 6 and detail & 0xFF == 7
     assert torch.equal(pg.orthogonalize(g), want)
     _check_status()
+
+
+def test_out_may_be_G_but_not_overlap_it():
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    buf = _gradient(65, 96, "flat", 1).bfloat16()
+    with pytest.raises(ValueError, match="overlaps G"):
+        pg.orthogonalize(buf[:64], buf[1:])
+    want = pg.orthogonalize(buf[:64])
+    assert torch.equal(pg.orthogonalize(buf[:64], buf[:64]), want)

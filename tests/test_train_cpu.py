@@ -26,6 +26,7 @@ def _forward(lib, rows=4, cols=8, x=256, ldx=8, dtype=0, w=256, b=256, wdtype=0,
     (dict(mean=None), INVALID), (dict(eps=-1e-5), INVALID), (dict(eps=float("nan")), INVALID),
     (dict(eps=float("inf")), INVALID), (dict(x=258), MISALIGNED), (dict(w=257, wdtype=1), MISALIGNED),
     (dict(y=513, dtype=1), MISALIGNED), (dict(mean=1026), MISALIGNED),
+    (dict(cols=(1 << 28) + 1, ldx=1 << 29, ldy=1 << 29), 3),
 ])
 def test_layer_norm_validation(lib, kw, status):
     assert _forward(lib, **kw) == status
