@@ -26,7 +26,7 @@
 //
 //   bfloat16 result:  A one pair, A A one, Q X two (one in the last step,
 //                     whose roundings no later step multiplies).
-//   float32 result:   A three pairs, A A three, Q X five (three in the last).
+//   float32 result:   A three pairs, A A three, Q X four (three in the last).
 //
 // Measured in float64 arithmetic on spectra from flat to 1e-3 of the largest
 // value (256 .. 1000 rows): the bfloat16 result is off by 1.03 to 1.15 times
@@ -67,7 +67,7 @@ enum Range { kAll, kRows, kCols };
 struct Pass {
     signed char left, right, range;
 };
-constexpr int kMaxPasses = 6;
+constexpr int kMaxPasses = 5;
 
 // The tensor cores add to a float32 accumulator by truncation: n additions in
 // a row lose about n 2^-25 of a sum of equal signs (A's diagonal), which a
@@ -1095,7 +1095,7 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
     const int kr = (l.r + BK - 1) / BK, kc = (l.c + BK - 1) / BK;
     const Cut cut_a = choose_cut(true, l.r, l.r, nb, (wide_result ? 3 : 1) * kc, fine, d);
     const Cut cut_s = choose_cut(true, l.r, l.r, nb, (wide_result ? 3 : 1) * kr + std::min(kr, 4), fine, d);
-    const Cut cut_x = choose_cut(false, l.r, l.c, nb, (wide_result ? 5 : 2) * kr + std::min(kr, 2), fine, d);
+    const Cut cut_x = choose_cut(false, l.r, l.c, nb, (wide_result ? 4 : 2) * kr + std::min(kr, 2), fine, d);
     CUtensorMap x_load[2], x_columns[2], a_load, a_diag_load, q_load, q_diag_load;
     CUtensorMap to_x[2], to_a[4], to_q[4], to_out; // a and q: store, mirror, store_diag, mirror_diag
     int st = GEMM_OK;
@@ -1244,10 +1244,8 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
         add(p, -1, 0, kRows);
         if (wide_result) {
             if (!one_plane) {
-                if (!last) {
+                if (!last)
                     add(p, 0, 2, kAll);
-                    add(p, 1, 1, kAll);
-                }
                 add(p, 0, 1, kAll);
             }
             add(p, 1, 0, kAll);

@@ -155,6 +155,8 @@ struct Call {
 // bfloat16 results of matrices whose shorter side is at most 128 and whose
 // longer one a cluster of eight CTAs holds (orthogonalize_small.cu).
 bool fits_small(int m, int n, int out_dtype);
+// Clusters of `ranks` CTAs, each alone on its SM, that run at once; 0 if unknown.
+int cluster_room(int ranks, const Device &d);
 int run_small(const Call &call, const Device &d, unsigned int *status, cudaStream_t s);
 
 } // namespace orth

@@ -9,13 +9,19 @@
 // or 8 CTAs, a cluster, hold a matrix.  The square and Q X need no exchange:
 // every CTA has all of A.  X X^T is summed over the CTAs' columns, each rank
 // adding the others' partial sums of its part in rank order and sending the
-// finished planes to all.
+// finished planes to all, in 4 KiB bulk copies.
 //
 // X lies as 64-column blocks of 128 rows of 128 bytes in the 128-byte swizzle:
 // K-major for X X^T, and the same bytes are the MN-major right operand of Q X.
 //
-// Measured on GB300 (microseconds a call, against orthogonalize.cu's kernels):
-// see the table at fits_small().
+// What bounds it is latency: five steps of three dependent products, each a
+// barrier, 8 to 24 MMAs, a wait and the accumulator's way through registers
+// back to shared memory, about 2.5 us together, and between the CTAs of a
+// cluster two exchanges a step.  The tensor cores work for a tenth of it.
+//
+// Measured on GB300, five steps, bfloat16 (microseconds a call; in brackets
+// orthogonalize.cu's kernels): 64 x 64 35, 128 x 128 43 (106), 128 x 256 51,
+// 100 x 512 66, 128 x 1024 72 (130), 2048 x 128 84; 16 of 100 x 300 82.
 #include <algorithm>
 
 #include "orthogonalize_internal.h"
@@ -27,17 +33,22 @@ namespace orth {
 constexpr int kSmallRows = 128;
 constexpr int kSlab = 256;     // columns of X that a CTA holds
 constexpr int kMaxRanks = 8;
-constexpr int kSmallThreads = 256;
+constexpr int kSmallThreads = 512;
 constexpr int kSmallSteps = 32;
 constexpr uint32_t kColumnBlock = kSmallRows * 128; // 64 columns: 16 KiB
-constexpr uint32_t kUnit = 32 * 64 * 4;             // a warp's share of a 128 x 128 sum
+constexpr uint32_t kUnit = 32 * 32 * 4;             // a warp's share of a 128 x 128 sum
+constexpr uint32_t kStrip = 32 * 128;               // 32 rows of a column block: one piece of a plane
 
-// Shared memory, from a 1024-byte boundary.
-constexpr uint32_t kX0 = 0, kX1 = 4 * kColumnBlock;                    // X's planes
-constexpr uint32_t kA0 = 8 * kColumnBlock, kA1 = 10 * kColumnBlock;    // A's, then Q's
-constexpr uint32_t kReceive = kA0;                                     // where the other ranks' sums arrive
-constexpr uint32_t kSmallSmem = 12 * kColumnBlock + 1024;
-static_assert(8 * kUnit <= 4 * kColumnBlock, "the sums fit where A and Q are not yet");
+// Shared memory, from a 1024-byte boundary: A's planes and then Q's, the other
+// ranks' sums, X's planes.  Four column blocks of X leave no room for the sums
+// beside A; they then arrive where A and Q are not yet, with two more meetings
+// of the cluster.
+constexpr uint32_t kA0 = 0, kA1 = 2 * kColumnBlock;
+constexpr uint32_t kBeside = 4 * kColumnBlock;
+constexpr int kRoomyBlocks = 3;
+constexpr uint32_t kSmallSmem = 14 * kColumnBlock + 1024;
+static_assert(16 * kUnit <= 4 * kColumnBlock, "the sums take no more than A's planes");
+static_assert(8 * kColumnBlock + kRoomyBlocks * 2 * kColumnBlock <= kSmallSmem - 1024, "X fits behind the sums");
 
 struct Small {
     Matrix g;
@@ -60,13 +71,12 @@ constexpr uint32_t instruction(int n, bool right_mn)
            (static_cast<uint32_t>(kSmallRows >> 4) << 24);
 }
 
-// 64 columns of this lane's row as one plane: in the 128-byte swizzle to
-// `row` (the row's 128 bytes of a column block), what it leaves over in v.
-__device__ __forceinline__ void make_plane(unsigned long long (&v)[32], uint32_t (&w)[32])
+// 32 columns of this lane's row as one plane; what it leaves over stays in v.
+__device__ __forceinline__ void make_plane(unsigned long long (&v)[16], uint32_t (&w)[16])
 {
     const unsigned long long minus = pair(-1.0f, -1.0f);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
+    for (int j = 0; j < 16; ++j) {
         float lo, hi;
         split(v[j], lo, hi);
         w[j] = pack_f16(lo, hi);
@@ -75,36 +85,38 @@ __device__ __forceinline__ void make_plane(unsigned long long (&v)[32], uint32_t
     }
 }
 
-__device__ __forceinline__ void store_plane(uint32_t row, int lane, const uint32_t (&w)[32], bool remote)
+// The same to `row`, a row's 128 bytes of a column block, its first or second
+// half, in the 128-byte swizzle.
+__device__ __forceinline__ void store_plane(uint32_t row, int lane, int second, const uint32_t (&w)[16])
 {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t at = row + static_cast<uint32_t>((j ^ (lane & 7)) << 4);
-        if (remote)
-            st_cluster_v4(at, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-        else
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(w[4 * j]), "r"(w[4 * j + 1]),
-                         "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
-                         : "memory");
-    }
+    for (int j = 0; j < 4; ++j)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(
+                         row + static_cast<uint32_t>(((second * 4 + j) ^ (lane & 7)) << 4)),
+                     "r"(w[4 * j]), "r"(w[4 * j + 1]), "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
+                     : "memory");
 }
 
 __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_constant__ Small p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2];
+    __shared__ __align__(8) uint64_t bars[3];
     __shared__ uint32_t tmem_slot;
     __shared__ float2 warp_sums[kSmallThreads / 32];
     __shared__ float2 rank_sums[kMaxRanks];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = align_smem(raw, 1024); // the same offset in every CTA of the cluster
-    const uint32_t done = smem_u32(&bars[0]), drained = smem_u32(&bars[1]);
+    const uint32_t done = smem_u32(&bars[0]), drained = smem_u32(&bars[1]), arrived = smem_u32(&bars[2]);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = p.ranks > 1 ? static_cast<int>(cluster_cta_rank()) : 0;
     const int b = static_cast<int>(blockIdx.x) / p.ranks;
     const int width = p.blocks * 64, col0 = rank * width; // this CTA's columns of X
-    const int quarter = warp & 3, half = warp >> 2;       // of the accumulators' rows and columns
+    const int quarter = warp & 3, part = warp >> 2;       // of the accumulators' rows and 32-column parts
     const int row = quarter * 32 + lane;
+    const bool roomy = p.blocks <= kRoomyBlocks;
+    const uint32_t receive = base + (roomy ? kBeside : kA0);
+    const uint32_t x0 = base + (roomy && p.ranks > 1 ? 2 * kBeside : kBeside);
+    const uint32_t x1 = x0 + static_cast<uint32_t>(p.blocks) * kColumnBlock;
     auto sync = [&]() {
         if (p.ranks > 1)
             cluster_sync();
@@ -115,6 +127,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     if (threadIdx.x == 0) {
         mbar_init(done, 1);
         mbar_init(drained, 1);
+        mbar_init(arrived, 1);
         fence_barrier_init();
     }
     if (warp == 0) {
@@ -203,7 +216,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
         for (int e = 0; e < 8; ++e)
             x[e] = v[e] * s0 * s1;
         for (int q = 0; q < (exact ? 1 : 2); ++q) {
-            const uint32_t plane = base + (q == 0 ? kX0 : kX1) + static_cast<uint32_t>(j / 64) * kColumnBlock;
+            const uint32_t plane = (q == 0 ? x0 : x1) + static_cast<uint32_t>(j / 64) * kColumnBlock;
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -256,25 +269,21 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
         tc_fence_after_sync();
         __syncwarp();
     };
-    // 64 columns of this thread's row of the accumulator at `column`.
-    auto read = [&](int column, unsigned long long (&v)[32]) {
-        uint32_t r0[32], r1[32];
-        const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(column);
-        tmem_ld_32x32b_x32(at, r0);
-        tmem_ld_32x32b_x32(at + 32u, r1);
+    // 32 columns of this thread's row of the accumulator at `column`.
+    auto read = [&](int column, unsigned long long (&v)[16]) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(column), r);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            v[j] = pair(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]));
-            v[16 + j] = pair(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]));
-        }
+        for (int j = 0; j < 16; ++j)
+            v[j] = pair(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
     };
-    // v alpha + diag I, for columns half * 64 .. of a 128 x 128 matrix.
-    auto scale = [&](unsigned long long (&v)[32], float alpha, float diag) {
+    // v alpha + diag I, for columns part * 32 .. of a 128 x 128 matrix.
+    auto scale = [&](unsigned long long (&v)[16], float alpha, float diag) {
         const unsigned long long a = pair(alpha, alpha);
-        const int at = row < p.r ? row - half * 64 : -1; // where the diagonal is among these columns
+        const int at = row < p.r ? row - part * 32 : -1; // where the diagonal is among these columns
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < 16; ++j)
             v[j] = fma2(v[j], a, pair(2 * j == at ? diag : 0.0f, 2 * j + 1 == at ? diag : 0.0f));
     };
     const int k_blocks = p.r > 64 ? 2 : 1; // of A and Q
@@ -285,7 +294,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     const uint64_t k_major = smem_desc_sw128(base, 16, 1024), mn_major = smem_desc_sw128(base, kColumnBlock, 1024);
     const uint32_t square_form = instruction(128, false), result_form = instruction(width, true);
     auto square_pass = [&](uint32_t on, uint32_t left, uint32_t right, int blocks, bool first) {
-        uint64_t l = k_major + (left >> 4), q = k_major + (right >> 4);
+        uint64_t l = k_major + ((left - base) >> 4), q = k_major + ((right - base) >> 4);
         for (int kb = 0; kb < blocks; ++kb, l += kBlockStep, q += kBlockStep) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
@@ -295,7 +304,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     };
     constexpr int kResult = 128; // accumulator of Q X, beside that of X X^T and the square
     auto result_pass = [&](uint32_t on, uint32_t left, uint32_t right, bool first) {
-        uint64_t l = k_major + (left >> 4), q = mn_major + (right >> 4);
+        uint64_t l = k_major + ((left - base) >> 4), q = mn_major + ((right - base) >> 4);
         for (int kb = 0; kb < k_blocks; ++kb, l += kBlockStep, q += 4 * kRowStep) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
@@ -309,21 +318,25 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
                     cc = p.coefficients[3 * step + 2];
         const bool first = step == 0, last = step == p.steps - 1;
         const float fs = first ? f : 1.0f;
-        unsigned long long v[32];
-        uint32_t w[32];
+        unsigned long long v[16];
+        uint32_t w[16];
 
         // X X^T, over all ranks' columns.
-        multiply([&](uint32_t on) { square_pass(on, kX0, kX0, p.blocks, true); });
-        read(half * 64, v);
-        const int unit = quarter * 2 + half, each = 8 / p.ranks, owner = unit / each;
+        multiply([&](uint32_t on) { square_pass(on, x0, x0, p.blocks, true); });
+        read(part * 32, v);
+        // Ranks own 128 / ranks columns' worth of rows: strips of 32 rows by
+        // 64 columns, eight of them, two warps each.
+        const int strip = quarter * 2 + part / 2, owner = strip * p.ranks / 8;
         if (p.ranks > 1) {
-            const uint32_t slots = base + kReceive + static_cast<uint32_t>(unit % each * p.ranks) * kUnit;
-            cluster_sync(); // no rank still multiplies by the Q that lies there
+            const uint32_t mine = static_cast<uint32_t>(strip % (8 / p.ranks) * 2 + (part & 1));
+            const uint32_t slots = receive + mine * static_cast<uint32_t>(p.ranks) * kUnit;
+            if (!roomy)
+                cluster_sync(); // no rank still multiplies by the Q that lies there
             if (owner != rank) {
                 const uint32_t to = map_to_cta(slots + static_cast<uint32_t>(rank) * kUnit,
                                                static_cast<uint32_t>(owner)) + static_cast<uint32_t>(lane) * 16u;
 #pragma unroll
-                for (int j = 0; j < 32; j += 2) {
+                for (int j = 0; j < 16; j += 2) {
                     float q0, q1, q2, q3;
                     split(v[j], q0, q1);
                     split(v[j + 1], q2, q3);
@@ -331,86 +344,102 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
                                   __float_as_uint(q2), __float_as_uint(q3));
                 }
             }
-            cluster_sync();
+            cluster_sync(); // also: no rank still multiplies by Q
             if (owner == rank) {
                 for (int src = 0; src < p.ranks; ++src) {
                     if (src == rank)
                         continue;
                     const uint8_t *from = smem_raw + (slots - raw) + src * kUnit + lane * 16;
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
+                    for (int j = 0; j < 16; j += 2) {
                         const float4 q = *reinterpret_cast<const float4 *>(from + j * 256);
                         v[j] = add2(v[j], pair(q.x, q.y));
                         v[j + 1] = add2(v[j + 1], pair(q.z, q.w));
                     }
                 }
             }
-            cluster_sync(); // the sums have been taken: A (or Q) may lie there
+            if (!roomy)
+                cluster_sync(); // the sums have been taken: A (or Q) may lie there
+            if (threadIdx.x == 0) // the strips the other ranks send, both planes
+                mbar_arrive_expect_tx(arrived, static_cast<uint32_t>(8 - 8 / p.ranks) * 2u * kStrip);
         }
         if (cc != 0.0f)
             scale(v, kScaleA / (kScaleX * kScaleX) * fs * fs, kScaleA * (cb / (2.0f * cc)));
         else
             scale(v, kScaleQ * cb / (kScaleX * kScaleX) * fs * fs * fs, kScaleQ * ca * fs);
-        const uint32_t row_at = static_cast<uint32_t>(half) * kColumnBlock + static_cast<uint32_t>(row) * 128u;
-        if (owner == rank || p.ranks == 1) {
+        const uint32_t row_at = static_cast<uint32_t>(part / 2) * kColumnBlock + static_cast<uint32_t>(row) * 128u;
+        if (owner == rank) {
             for (int q = 0; q < 2; ++q) {
                 make_plane(v, w);
-                const uint32_t to = base + (q == 0 ? kA0 : kA1) + row_at;
-                if (p.ranks == 1)
-                    store_plane(to, lane, w, false);
-                else
-                    for (int k = 0; k < p.ranks; ++k)
-                        store_plane(map_to_cta(to, static_cast<uint32_t>(k)), lane, w, true);
+                store_plane(base + (q == 0 ? kA0 : kA1) + row_at, lane, part & 1, w);
             }
         }
-        if (p.ranks > 1)
-            cluster_sync();
+        if (p.ranks > 1) {
+            // Each strip, 4 KiB in one piece, to every other rank.
+            fence_proxy_async_smem();
+            __syncthreads();
+            if (owner == rank && (part & 1) == 0 && lane < 2 * p.ranks) {
+                const uint32_t at = base + (lane & 1 ? kA1 : kA0) + static_cast<uint32_t>(part / 2) * kColumnBlock +
+                                    static_cast<uint32_t>(quarter * 32) * 128u;
+                const uint32_t to = static_cast<uint32_t>(lane / 2);
+                if (to != static_cast<uint32_t>(rank))
+                    bulk_copy_to_cta(map_to_cta(at, to), at, kStrip, map_to_cta(arrived, to));
+            }
+            // Also after a product's wait ran out: no rank leaves before the
+            // copies to it have landed.
+            if (!mbar_wait_bounded(arrived, static_cast<uint32_t>(step & 1), p.wait_limit_ns) && !failed) {
+                failed = true;
+                record_error(p.status, kErrFamilyOrthogonalize | kErrRoleConsumer);
+            }
+            cluster_arrive(); // this rank has them: the copies to it no longer read their source
+        }
 
         if (cc != 0.0f) {
             // The square, in every rank, and Q in A's place.
             multiply([&](uint32_t on) {
-                square_pass(on, kA1, kA0, k_blocks, true);
-                square_pass(on, kA0, kA1, k_blocks, false);
-                square_pass(on, kA0, kA0, k_blocks, false);
+                square_pass(on, base + kA1, base + kA0, k_blocks, true);
+                square_pass(on, base + kA0, base + kA1, k_blocks, false);
+                square_pass(on, base + kA0, base + kA0, k_blocks, false);
             });
-            read(half * 64, v);
+            read(part * 32, v);
             scale(v, kScaleQ * cc / (kScaleA * kScaleA) * fs,
                   kScaleQ * static_cast<float>(ca - static_cast<double>(cb) * cb / (4.0 * cc)) * fs);
+            if (p.ranks > 1)
+                cluster_wait(); // before Q replaces the strips this rank has sent
             for (int q = 0; q < 2; ++q) {
                 make_plane(v, w);
-                store_plane(base + (q == 0 ? kA0 : kA1) + row_at, lane, w, false);
+                store_plane(base + (q == 0 ? kA0 : kA1) + row_at, lane, part & 1, w);
             }
+        } else if (p.ranks > 1) {
+            cluster_wait();
         }
 
         // Q X: this rank's columns, in X's place or to the result.
         multiply([&](uint32_t on) {
-            result_pass(on, kA1, kX0, true);
+            result_pass(on, base + kA1, x0, true);
             if (!last && !(first && exact))
-                result_pass(on, kA0, kX1, false);
-            result_pass(on, kA0, kX0, false);
+                result_pass(on, base + kA0, x1, false);
+            result_pass(on, base + kA0, x0, false);
         });
-        for (int k = 0; k < 2; ++k) {
-            const int block = half * 2 + k;
-            if (block >= p.blocks)
-                break; // warp-uniform
-            read(kResult + block * 64, v);
+        for (int k = part; k < 2 * p.blocks; k += 4) { // 32 columns each
+            read(kResult + k * 32, v);
             const float alpha = last ? 1.0f / (kScaleQ * kScaleX) : 1.0f / kScaleQ;
             const unsigned long long a2 = pair(alpha, alpha);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < 16; ++j)
                 v[j] = mul2(v[j], a2);
             if (!last) {
                 for (int q = 0; q < 2; ++q) {
                     make_plane(v, w);
-                    store_plane(base + (q == 0 ? kX0 : kX1) + static_cast<uint32_t>(block) * kColumnBlock +
-                                    static_cast<uint32_t>(row) * 128u, lane, w, false);
+                    store_plane((q == 0 ? x0 : x1) + static_cast<uint32_t>(k / 2) * kColumnBlock +
+                                    static_cast<uint32_t>(row) * 128u, lane, k & 1, w);
                 }
             } else if (row < p.r) {
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + b * p.out_batch;
-                const int j0 = col0 + block * 64;
+                const int j0 = col0 + k * 32;
                 if (p.tall) { // neighbouring lanes write neighbours
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) {
+                    for (int j = 0; j < 32; ++j) {
                         float lo, hi;
                         split(v[j / 2], lo, hi);
                         if (j0 + j < p.c)
@@ -419,7 +448,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
                 } else {
                     __nv_bfloat16 *o = out + row * p.ldo + j0;
 #pragma unroll
-                    for (int j = 0; j < 64; j += 8) {
+                    for (int j = 0; j < 32; j += 8) {
                         float q[8];
 #pragma unroll
                         for (int e = 0; e < 8; e += 2)
@@ -455,12 +484,21 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
         tmem_dealloc(tmem, 512);
 }
 
-// CTAs of a matrix whose longer side is c, and 64-column blocks of each.
-static int ranks_for(int c, int *blocks)
+// CTAs of a matrix whose longer side is c, and 64-column blocks of each.  A
+// cluster whose CTAs hold at most three blocks saves two meetings a step: one
+// 128 x 1024 matrix takes 71.9 us on eight CTAs, 78.1 on four.  So a cluster
+// grows to that where all matrices still run at once; 64 such matrices, which
+// would take five rounds of eight CTAs, take 361 us so and 167 on four.
+static int ranks_for(int c, int batch, const Device &d, int *blocks)
 {
     int ranks = 1;
     while (ranks < kMaxRanks && c > ranks * kSlab)
         ranks *= 2;
+    int more = ranks;
+    while (more > 1 && more < kMaxRanks && c > more * kRoomyBlocks * 64)
+        more *= 2;
+    if (more > ranks && batch <= cluster_room(more, d))
+        ranks = more;
     *blocks = (c + 64 * ranks - 1) / (64 * ranks);
     return ranks;
 }
@@ -478,7 +516,7 @@ int run_small(const Call &call, const Device &d, unsigned int *status, cudaStrea
     p.r = std::min(call.m, call.n);
     p.c = std::max(call.m, call.n);
     p.tall = call.m > call.n;
-    p.ranks = ranks_for(p.c, &p.blocks);
+    p.ranks = ranks_for(p.c, call.batch, d, &p.blocks);
     p.out = call.out;
     p.ldo = call.ldo;
     p.out_batch = call.o_batch;

@@ -259,6 +259,19 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
+// Its two halves, for work between them.
+__device__ __forceinline__ void cluster_arrive()
+{
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait()
+{
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+
 // The address, in the cluster's shared memory, of CTA `rank`'s counterpart of
 // this CTA's shared address, and a 16-byte store to such an address.
 __device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t rank)
@@ -277,6 +290,17 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_
 __device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_t b)
 {
     asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};\n" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
+// Bulk copy of this CTA's shared memory at `src` to an address of another CTA
+// of the cluster, completing on a barrier of that one (both from map_to_cta);
+// 16-byte aligned, a multiple of 16 bytes.
+__device__ __forceinline__ void bulk_copy_to_cta(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                     dst),
+                 "r"(src), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
 // Record the first error of this launch sequence in the device status word.
