@@ -187,13 +187,14 @@ Plan spread(int rows, int cols, int e, int max_threads, int streams, int paramet
     const int groups = std::max(1, std::min(max_threads / tpr, (rows + ctas - 1) / ctas));
     const int trips = (rows + groups - 1) / groups;
     const int row_bytes = cols * static_cast<int>(size);
-    const int slot_bytes = vectors ? row_bytes : (row_bytes + 15 + 15) / 16 * 16;
+    // An unaligned row's last piece is read with the granule after it.
+    const int slot_bytes = vectors ? row_bytes : (row_bytes + 15 + 15) / 16 * 16 + 16;
     const int fixed = parameters * parameter_floats(cols) * 4;
     const int layer = groups * streams * slot_bytes; // one slot of every group
     const int slots = std::min({kMaxSlots, std::max(2, kRingBytes / layer), (kSmemBytes - fixed) / layer});
     const bool ring = trips > 2 * ctas && slots >= 2;
     plan.source = !ring ? (vectors ? kVector : kScalar)
-                  : !vectors ? kRingScalar
+                  : !vectors ? kRingShifted
                   : cols == tpr * e && full ? kRingFull : kRingVector;
     plan.shape = Shape{tpr, groups, slots, slot_bytes, d.status, call_wait_limit_ns(), call_withhold()};
     plan.grid = std::min(trips, ctas);
@@ -217,8 +218,10 @@ int launch_forward(const Forward &p, const Device &d, cudaStream_t s)
                          vector_parameter(p.bias);
     // 16 elements a thread give a single row the most threads; 32 give many
     // rows the most groups, whose reductions overlap.
-    const int e = p.cols <= 512 || ((p.rows <= 2 * d.sms || !vectors) && p.cols <= 8192) ? 16 : 32;
+    const int e = p.cols <= 512 || (p.rows <= 2 * d.sms && p.cols <= 8192) ? 16 : 32;
     Plan plan = spread(p.rows, p.cols, e, forward_threads(e), 1, 2, vectors, true, sizeof(T), d, d.sms);
+    if (plan.source == kScalar && e == 32 && p.cols <= 8192)
+        plan = spread(p.rows, p.cols, 16, forward_threads(16), 1, 2, vectors, true, sizeof(T), d, d.sms);
     if (plan.elements != 0) {
         if (!from_ring(plan.source)) // no ring to keep the memory system busy: every CTA that fits
             plan.grid = std::min((p.rows + plan.shape.groups - 1) / plan.shape.groups, 4 * d.sms);

@@ -27,13 +27,21 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) backward_rows_kernel(cons
     float *weight = reinterpret_cast<float *>(smem);
     uint8_t *slots = smem + (kRing ? parameter_floats(p.cols) * 4 : 0);
     Ring<2> ring(smem_u32(bars), smem_u32(slots), shape, g, p.cols * static_cast<int>(sizeof(T)), p.rows);
-    const uint8_t *own = slots + (ring.slots_at - smem_u32(slots));
+    uint8_t *own = slots + (ring.slots_at - smem_u32(slots));
     if constexpr (kRing) {
         ring.in[0] = Stream{static_cast<const uint8_t *>(p.x), p.ldx * static_cast<long long>(sizeof(T))};
         ring.in[1] = Stream{static_cast<const uint8_t *>(p.dy), p.lddy * static_cast<long long>(sizeof(T))};
         ring.init();
         ring.start(); // a thread's own copies on its own mbarriers; the others meet them past the barrier
-        at.copy_parameter(weight, p.weight, p.weight_bf16, 1.0f, p.cols);
+        at.copy_parameter(weight, p.weight, p.weight_bf16, 1.0f);
+    }
+    const long long step = static_cast<long long>(gridDim.x) * shape.groups;
+    const long long first = static_cast<long long>(blockIdx.x) * shape.groups + g.index;
+    Edges<T, 2> edges;
+    if constexpr (S == kRingShifted) {
+        edges.load(ring, g, first);
+        edges.place(ring, own, 0);
+        edges.load(ring, g, first + step);
     }
     __syncthreads();
     unsigned long long dw[E / 2], db[E / 2];
@@ -48,8 +56,6 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) backward_rows_kernel(cons
             at.load_parameter_piece(p.weight, p.weight_bf16, 1.0f, k, v);
     };
 
-    const long long step = static_cast<long long>(gridDim.x) * shape.groups;
-    const long long first = static_cast<long long>(blockIdx.x) * shape.groups + g.index;
     float next_mean = 0.0f, next_rstd = 0.0f; // loaded a row ahead
     if (first < p.rows) {
         next_mean = p.mean[first];
@@ -57,6 +63,10 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) backward_rows_kernel(cons
     }
     // The bound is the same in the whole group.
     for (long long row = first; row < p.rows; row += step) {
+        if constexpr (S == kRingShifted) {
+            edges.place(ring, own, ring.slot + 1 == ring.slots ? 0 : ring.slot + 1);
+            edges.load(ring, g, row + 2 * step);
+        }
         const float mean = next_mean, rstd = next_rstd;
         if (row + step < p.rows) {
             next_mean = p.mean[row + step];
@@ -68,10 +78,10 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) backward_rows_kernel(cons
             x = ring.template view<T>(own, 0, row);
             dy = ring.template view<T>(own, 1, row);
         } else {
-            x.near = static_cast<const T *>(p.x) + row * p.ldx;
-            dy.near = static_cast<const T *>(p.dy) + row * p.lddy;
+            x.at = static_cast<const T *>(p.x) + row * p.ldx;
+            dy.at = static_cast<const T *>(p.dy) + row * p.lddy;
         }
-        T *dx = static_cast<T *>(p.dx) + row * p.lddx;
+        RowOut<T, E, S> dx(at, static_cast<T *>(p.dx) + row * p.lddx);
         const unsigned long long minus = pair(-mean, -mean), scale = pair(rstd, rstd);
         // Two chains of paired additions for each sum.
         unsigned long long s1[2] = {0ull, 0ull}, s2[2] = {0ull, 0ull};
@@ -111,7 +121,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) backward_rows_kernel(cons
                 split(mul2(add2(fma2(xhat[j], m2, t[j]), m1), scale), v[2 * j], v[2 * j + 1]);
 #pragma unroll
             for (int k = 0; k < kPieces; ++k)
-                at.store_piece(dx, k, v + k * kPiece);
+                dx.put(k, v + k * kPiece);
+            dx.finish();
         } else {
             constexpr int kStep = kPiece == 1 ? 2 : kPiece; // elements at a time: whole pairs
             auto load = [&](int i, float (&xv)[kStep], float (&gv)[kStep], float (&wv)[kStep]) {
@@ -149,8 +160,9 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) backward_rows_kernel(cons
                 }
 #pragma unroll
                 for (int e = 0; e < kStep; e += kPiece)
-                    at.store_piece(dx, (i + e) / kPiece, v + e);
+                    dx.put((i + e) / kPiece, v + e);
             }
+            dx.finish();
             if constexpr (kRing) {
                 g.barrier();
                 ring.next();
@@ -173,7 +185,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) backward_rows_kernel(cons
         const bool last = k == shape.groups - 1;
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            if (!at.has(i / kPiece))
+            if (!at.has(i / kPiece, i % kPiece))
                 break;
             const int j = at.column(i / kPiece) + i % kPiece;
             float lo, hi;
@@ -222,7 +234,7 @@ static int launch_source(const Backward &p, const Plan &plan, const Device &d, c
             return launch<T, E, kRingFull>(p, plan, d, s);
     switch (plan.source) {
     case kRingVector: return launch<T, E, kRingVector>(p, plan, d, s);
-    case kRingScalar: return launch<T, E, kRingScalar>(p, plan, d, s);
+    case kRingShifted: return launch<T, E, kRingShifted>(p, plan, d, s);
     case kVector: return launch<T, E, kVector>(p, plan, d, s);
     default: return launch<T, E, kScalar>(p, plan, d, s);
     }

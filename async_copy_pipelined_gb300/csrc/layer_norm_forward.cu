@@ -21,20 +21,31 @@ __global__ void __launch_bounds__(forward_threads(E), 1) forward_rows_kernel(con
     float *weight = reinterpret_cast<float *>(smem), *bias = weight + parameter_floats(p.cols);
     uint8_t *slots = smem + (kRing ? 2 * parameter_floats(p.cols) * 4 : 0);
     Ring<1> ring(smem_u32(bars), smem_u32(slots), shape, g, p.cols * static_cast<int>(sizeof(T)), p.rows);
-    const uint8_t *own = slots + (ring.slots_at - smem_u32(slots));
+    uint8_t *own = slots + (ring.slots_at - smem_u32(slots));
     if constexpr (kRing) {
         ring.in[0] = Stream{static_cast<const uint8_t *>(p.x), p.ldx * static_cast<long long>(sizeof(T))};
         ring.init();
         ring.start(); // a thread's own copies on its own mbarriers; the others meet them past the barrier
-        at.copy_parameter(weight, p.weight, p.weight_bf16, 1.0f, p.cols);
-        at.copy_parameter(bias, p.bias, p.weight_bf16, 0.0f, p.cols);
+        at.copy_parameter(weight, p.weight, p.weight_bf16, 1.0f);
+        at.copy_parameter(bias, p.bias, p.weight_bf16, 0.0f);
+    }
+    const long long step = static_cast<long long>(gridDim.x) * shape.groups;
+    const long long first = static_cast<long long>(blockIdx.x) * shape.groups + g.index;
+    Edges<T, 1> edges;
+    if constexpr (S == kRingShifted) {
+        edges.load(ring, g, first);
+        edges.place(ring, own, 0);
+        edges.load(ring, g, first + step);
     }
     __syncthreads();
     const float n = static_cast<float>(p.cols), inv = 1.0f / n;
 
-    const long long step = static_cast<long long>(gridDim.x) * shape.groups;
     // The bound is the same in the whole group.
-    for (long long row = static_cast<long long>(blockIdx.x) * shape.groups + g.index; row < p.rows; row += step) {
+    for (long long row = first; row < p.rows; row += step) {
+        if constexpr (S == kRingShifted) {
+            edges.place(ring, own, ring.slot + 1 == ring.slots ? 0 : ring.slot + 1);
+            edges.load(ring, g, row + 2 * step);
+        }
         unsigned long long d[E / 2];
         // Without a ring, and while registers allow, weight and bias are loaded
         // beside x: a single row waits for memory once.
@@ -47,7 +58,7 @@ __global__ void __launch_bounds__(forward_threads(E), 1) forward_rows_kernel(con
                 at.load(ring.template view<T>(own, 0, row), x);
             } else {
                 const T *from = static_cast<const T *>(p.x) + row * p.ldx;
-                at.load(Row<T>{from, from, 0, p.cols}, x);
+                at.load(Row<T>{from, 0}, x);
                 if constexpr (kEarly) {
 #pragma unroll
                     for (int k = 0; k < kPieces; ++k) {
@@ -79,7 +90,7 @@ __global__ void __launch_bounds__(forward_threads(E), 1) forward_rows_kernel(con
             part[i & 1] = fma2(d[i], d[i], part[i & 1]);
         const float rstd = rsqrtf(fmaf(g.sum(both(add2(part[0], part[1]))), inv, p.eps));
         const unsigned long long scale = pair(rstd, rstd);
-        T *y = static_cast<T *>(p.y) + row * p.ldy;
+        RowOut<T, E, S> y(at, static_cast<T *>(p.y) + row * p.ldy);
         auto parameters = [&](int k, float *wk, float *bk) {
             if constexpr (kRing) {
                 at.load_copy_piece(weight, p.cols, k, wk);
@@ -102,7 +113,7 @@ __global__ void __launch_bounds__(forward_threads(E), 1) forward_rows_kernel(con
                 parameters(k, &wk, &bk);
                 split(d[k / 2], lo, hi);
                 const float v = fmaf((k & 1 ? hi : lo) * rstd, wk, bk);
-                at.store_piece(y, k, &v);
+                y.put(k, &v);
             }
         } else {
 #pragma unroll
@@ -115,8 +126,9 @@ __global__ void __launch_bounds__(forward_threads(E), 1) forward_rows_kernel(con
                                                       pair(bk[e], bk[e + 1]));
                     split(r, v[e], v[e + 1]);
                 }
-                at.store_piece(y, k, v);
+                y.put(k, v);
             }
+            y.finish();
         }
         if (p.mean && g.t == 0) {
             p.mean[row] = mean;
@@ -146,7 +158,7 @@ static int launch_source(const Forward &p, const Plan &plan, const Device &d, cu
     switch (plan.source) {
     case kRingFull: return launch<T, E, kRingFull>(p, plan, d, s);
     case kRingVector: return launch<T, E, kRingVector>(p, plan, d, s);
-    case kRingScalar: return launch<T, E, kRingScalar>(p, plan, d, s);
+    case kRingShifted: return launch<T, E, kRingShifted>(p, plan, d, s);
     case kVector: return launch<T, E, kVector>(p, plan, d, s);
     default: return launch<T, E, kScalar>(p, plan, d, s);
     }

@@ -53,9 +53,6 @@ struct Plan {
 constexpr int forward_threads(int elements) { return elements > 16 ? 512 : 768; }
 constexpr int kBackwardThreads = 512;
 
-// Floats that a parameter's copy in shared memory takes (a multiple of 16 bytes).
-__host__ __device__ constexpr int parameter_floats(int cols) { return (cols + 3) / 4 * 4; }
-
 struct Device {
     int index, sms;
     unsigned long long ctx;

@@ -2,8 +2,10 @@
 // its sums are formed, and the ring through which rows reach shared memory.
 //
 // A group of `tpr` threads (whole warps) takes a row, each thread E of its
-// elements in registers; a CTA holds `groups` groups.  Rows that are 16-byte
-// aligned move in 16-byte vectors, others element by element.
+// elements in registers; a CTA holds `groups` groups.  Elements move in 16-byte
+// vectors: straight where the rows are 16-byte aligned; where they are not,
+// through shared memory and shifted (kRingShifted), or, when there are too few
+// rows for a ring, one by one.
 //
 // Ring: the first thread of each group copies the group's rows into shared
 // memory (bulk copies completing on mbarriers), several ahead of the one being
@@ -39,9 +41,17 @@ constexpr int kRingBytes = 128 * 1024;
 // the thread's own; 16-byte vectors, or single elements.
 // kRingFull: vectors from the ring in rows of exactly tpr E elements, so that
 // no piece needs asking whether it is there.
-enum Source { kRingFull, kRingVector, kRingScalar, kVector, kScalar };
-constexpr bool from_ring(Source s) { return s == kRingFull || s == kRingVector || s == kRingScalar; }
-constexpr bool in_vectors(Source s) { return s == kRingFull || s == kRingVector || s == kVector; }
+// kRingShifted: rows of any alignment and length.  A piece is cut out of the
+// two 16-byte granules of shared memory it lies in, and a warp's pieces are
+// shifted against each other to the granules of the output: 8192 rows of 8192
+// bfloat16 at a pitch of 8195 take 69 us forward and 122 backward, 142 and 193
+// element by element; in float32 89 and 176, 128 and 164 element by element.
+enum Source { kRingFull, kRingVector, kRingShifted, kVector, kScalar };
+constexpr bool from_ring(Source s) { return s == kRingFull || s == kRingVector || s == kRingShifted; }
+constexpr bool in_vectors(Source s) { return s != kScalar; }
+
+// Floats that a parameter's copy in shared memory takes: whole pieces.
+__host__ __device__ constexpr int parameter_floats(int cols) { return (cols + 7) / 8 * 8; }
 
 struct Shape {
     int tpr, groups; // threads per row; rows at a time in a CTA
@@ -68,13 +78,29 @@ __device__ __forceinline__ float warp_sum(float v)
 }
 
 // ------------------------------------------------------------ a row's elements
-// A row where a thread finds it: elements head .. tail-1 at `near` (shared
-// memory, or the row itself), the others at `far` (the row in global memory).
+// A row where a thread finds it: in shared memory or in global memory.
 template <class T>
 struct Row {
-    const T *near, *far;
-    int head, tail;
+    const T *at;
+    int lead; // bytes of its first granule before it (kRingShifted)
 };
+
+// The sixteen bytes at byte s of a and b in a row; s below 16, a whole number
+// of T.  By selections: branching on the row's s instead took a third longer
+// in float32, whose registers then spill.
+template <class T>
+__device__ __forceinline__ uint4 window(const uint4 &a, const uint4 &b, int s)
+{
+    const bool two = s & 8, one = s & 4;
+    const uint32_t c0 = two ? a.z : a.x, c1 = two ? a.w : a.y, c2 = two ? b.x : a.z, c3 = two ? b.y : a.w,
+                   c4 = two ? b.z : b.x, c5 = two ? b.w : b.y;
+    const uint32_t d0 = one ? c1 : c0, d1 = one ? c2 : c1, d2 = one ? c3 : c2, d3 = one ? c4 : c3;
+    if constexpr (sizeof(T) == 4)
+        return make_uint4(d0, d1, d2, d3);
+    const uint32_t d4 = one ? c5 : c4, bits = (s & 2) * 8;
+    return make_uint4(__funnelshift_r(d0, d1, bits), __funnelshift_r(d1, d2, bits), __funnelshift_r(d2, d3, bits),
+                      __funnelshift_r(d3, d4, bits));
+}
 
 // Where a thread has its elements: warp w of a group takes 32 E columns in a
 // row, piece k (a vector, or one element) of its lane l starting at column
@@ -84,28 +110,42 @@ struct Spread {
     static constexpr int kPiece = in_vectors(S) ? Vec16<T>::kElements : 1;
     static constexpr int kPieces = E / kPiece;
     int first;  // column of piece 0
-    int pieces; // of this thread that lie in the row (a vector row has whole vectors only)
-    bool full;  // every lane of the warp has all of them
+    int cols;
+    int pieces; // of this thread that lie in the row (kRingShifted: the last perhaps in part)
+    bool full;  // every lane of the warp has all of them, whole
 
-    __device__ __forceinline__ Spread(int t, int cols) : first(t / 32 * 32 * E + t % 32 * kPiece)
+    __device__ __forceinline__ Spread(int t, int cols_) : first(t / 32 * 32 * E + t % 32 * kPiece), cols(cols_)
     {
         const int left = (cols - first + 32 * kPiece - 1) / (32 * kPiece);
         pieces = cols > first ? (left < kPieces ? left : kPieces) : 0;
-        full = __all_sync(0xffffffffu, pieces == kPieces);
+        const bool whole = S != kRingShifted || column(kPieces - 1) + kPiece <= cols;
+        full = __all_sync(0xffffffffu, pieces == kPieces && whole);
     }
     __device__ __forceinline__ int column(int k) const { return first + k * (32 * kPiece); }
     __device__ __forceinline__ bool has(int k) const { return S == kRingFull || k < pieces; }
+    // Element e of piece k.
+    __device__ __forceinline__ bool has(int k, int e) const
+    {
+        return S == kRingShifted ? column(k) + e < cols : has(k);
+    }
 
     __device__ __forceinline__ void load_piece(const Row<T> &row, int k, float *v) const
     {
-        if (has(k)) {
+        if constexpr (S == kRingShifted) {
+            const uint4 *q = reinterpret_cast<const uint4 *>(
+                reinterpret_cast<const uint8_t *>(row.at + (has(k) ? column(k) : 0)) - row.lead);
+            Vec16<T>::unpack(window<T>(q[0], q[1], row.lead), v);
+            if (!full) {
+#pragma unroll
+                for (int e = 0; e < kPiece; ++e)
+                    v[e] = has(k, e) ? v[e] : 0.0f;
+            }
+        } else if (has(k)) {
             const int j = column(k);
-            if constexpr (S == kRingScalar)
-                v[0] = to_f32(j >= row.head && j < row.tail ? row.near[j] : row.far[j]);
-            else if constexpr (S == kScalar)
-                v[0] = to_f32(row.near[j]);
+            if constexpr (S == kScalar)
+                v[0] = to_f32(row.at[j]);
             else
-                Vec16<T>::unpack(*reinterpret_cast<const uint4 *>(row.near + j), v);
+                Vec16<T>::unpack(*reinterpret_cast<const uint4 *>(row.at + j), v);
         } else {
 #pragma unroll
             for (int e = 0; e < kPiece; ++e)
@@ -127,9 +167,9 @@ struct Spread {
         for (int i = 0; i < E / 2; ++i) {
             float a, b;
             split(v[i], a, b);
-            if (2 * i / kPiece >= pieces)
+            if (!has(2 * i / kPiece, 2 * i % kPiece))
                 a = 0.0f;
-            if ((2 * i + 1) / kPiece >= pieces)
+            if (!has((2 * i + 1) / kPiece, (2 * i + 1) % kPiece))
                 b = 0.0f;
             v[i] = pair(a, b);
         }
@@ -176,25 +216,25 @@ struct Spread {
     // Absent pieces read the first.
     __device__ __forceinline__ void load_copy_piece(const float *copy, int cols, int k, float *v) const
     {
-        const int j = has(k) ? column(k) : 0;
+        const int j = has(k) ? column(k) : 0, half = S == kRingShifted ? parameter_floats(cols) / 2 : cols / 2;
         if constexpr (kPiece == 8) {
             Vec16<float>::unpack(*reinterpret_cast<const uint4 *>(copy + j / 2), v);
-            Vec16<float>::unpack(*reinterpret_cast<const uint4 *>(copy + cols / 2 + j / 2), v + 4);
-        } else if constexpr (kPiece == 4) {
-            Vec16<float>::unpack(*reinterpret_cast<const uint4 *>(copy + j), v);
+            Vec16<float>::unpack(*reinterpret_cast<const uint4 *>(copy + half + j / 2), v + 4);
         } else {
-            v[0] = copy[j];
+            Vec16<float>::unpack(*reinterpret_cast<const uint4 *>(copy + j), v);
         }
     }
     // A parameter vector as float32 in shared memory, by the whole CTA.  For
     // pieces of eight the first halves of all pieces come before the second
-    // halves, so that neighbouring threads' 16-byte reads are neighbours.
-    static __device__ __forceinline__ void copy_parameter(float *copy, const void *p, bool bf16, float absent, int cols)
+    // halves, so that neighbouring threads' 16-byte reads are neighbours.  What
+    // a last piece has beyond the row is `absent` too: it meets zeros, and must
+    // be finite.
+    __device__ __forceinline__ void copy_parameter(float *copy, const void *p, bool bf16, float absent) const
     {
         // Several loads of a thread in flight: the first rows wait for them.
-        constexpr int kUnit = in_vectors(S) ? 4 : 1, kBatch = 8;
-        const int units = cols / kUnit;
-        for (int u0 = threadIdx.x; u0 < units; u0 += kBatch * blockDim.x) {
+        constexpr int kUnit = S == kRingShifted ? 1 : 4, kBatch = 8;
+        const int half = parameter_floats(cols) / 2, there = S == kRingShifted ? 2 * half : cols;
+        for (int u0 = threadIdx.x; u0 < there / kUnit; u0 += kBatch * blockDim.x) {
             float v[kBatch][kUnit];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
@@ -219,13 +259,88 @@ struct Spread {
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const int j = (u0 + k * static_cast<int>(blockDim.x)) * kUnit;
-                if (j < cols) {
+                if (j < there) {
+                    float *to = copy + (kPiece == 8 ? (j & 4 ? half : 0) + j / 8 * 4 + j % 4 : j);
                     if constexpr (kUnit == 1)
-                        copy[j] = v[k][0];
+                        *to = v[k][0];
                     else
-                        *reinterpret_cast<uint4 *>(copy + (kPiece == 8 ? (j & 4 ? cols / 2 : 0) + j / 8 * 4 : j)) =
-                            Vec16<float>::pack(v[k]);
+                        *reinterpret_cast<uint4 *>(to) = Vec16<float>::pack(v[k]);
                 }
+            }
+        }
+    }
+};
+
+// A row of the output, written piece by piece: put() for every piece in turn,
+// then finish(), by whole warps.  kRingShifted: where the row starts `off`
+// bytes into a granule, a lane writes the granule in which its piece begins,
+// whose first `off` bytes are the end of the piece before: the lane's before
+// it, or for the first lane the last lane's of the round before.  What lies in
+// granules that two warps share goes element by element.
+template <class T, int E, Source S>
+struct RowOut {
+    using At = Spread<T, E, S>;
+    const At &at;
+    T *row;
+    int off;
+    uint4 edge = {}; // the first lane's first piece, the last lane's last
+
+    __device__ __forceinline__ RowOut(const At &at_, T *row_)
+        : at(at_), row(row_), off(static_cast<int>(reinterpret_cast<uintptr_t>(row_) & 15u))
+    {
+    }
+    // Elements from .. to-1 of q, whose element 0 belongs to column j.
+    __device__ __forceinline__ void elements(const uint4 &q, int j, int from, int to) const
+    {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int e = 0; e < At::kPiece; ++e) {
+            if (e < from || e >= to)
+                continue;
+            if constexpr (sizeof(T) == 4)
+                row[j + e] = __uint_as_float(w[e]);
+            else
+                row[j + e] = __ushort_as_bfloat16(static_cast<unsigned short>(w[e / 2] >> (16 * (e & 1))));
+        }
+    }
+    __device__ __forceinline__ void put(int k, const float *v)
+    {
+        if constexpr (S != kRingShifted) {
+            at.store_piece(row, k, v);
+        } else {
+            const uint4 q = Vec16<T>::pack(v);
+            const int lane = static_cast<int>(threadIdx.x) & 31;
+            int j = at.column(k), from = 0;
+            uint4 out = q;
+            if (off != 0) {
+                const uint4 sent = lane == 31 ? edge : q;
+                uint4 before;
+                before.x = __shfl_sync(0xffffffffu, sent.x, (lane + 31) & 31);
+                before.y = __shfl_sync(0xffffffffu, sent.y, (lane + 31) & 31);
+                before.z = __shfl_sync(0xffffffffu, sent.z, (lane + 31) & 31);
+                before.w = __shfl_sync(0xffffffffu, sent.w, (lane + 31) & 31);
+                out = window<T>(before, q, 16 - off);
+                j -= off / static_cast<int>(sizeof(T));
+                if (lane == 0 ? k == 0 : lane == 31)
+                    edge = q;
+                if (k == 0 && lane == 0)
+                    from = At::kPiece; // finish() writes it
+            }
+            const int to = at.cols - j;
+            if (from == 0 && to >= At::kPiece)
+                *reinterpret_cast<uint4 *>(row + j) = out;
+            else if (from == 0 && to > 0)
+                elements(out, j, 0, to);
+        }
+    }
+    __device__ __forceinline__ void finish() const
+    {
+        if constexpr (S == kRingShifted) {
+            const int lane = static_cast<int>(threadIdx.x) & 31;
+            if (off != 0 && (lane == 0 || lane == 31)) {
+                const int cut = At::kPiece - off / static_cast<int>(sizeof(T));
+                const int j = at.column(lane == 0 ? 0 : At::kPieces - 1), left = at.cols - j;
+                elements(edge, j, lane == 0 ? 0 : cut, lane == 0 ? min(cut, left) : left);
             }
         }
     }
@@ -317,7 +432,7 @@ struct Stream {
 // A group's ring: position i (its row first + i step) uses slot i % slots.
 // Only whole 16-byte granules of a row are copied, to the offset in the slot
 // that they have in global memory; what is left of an unaligned row at its two
-// ends its threads read themselves.  A wait that runs out is recorded once;
+// ends follows through registers (Edges).  A wait that runs out is recorded once;
 // from then on the thread neither waits nor fills, and its group's barriers
 // stay matched.
 template <int Streams>
@@ -406,15 +521,8 @@ struct Ring {
     template <class T>
     __device__ __forceinline__ Row<T> view(const uint8_t *own, int i, long long r) const
     {
-        const uint8_t *far = in[i].base + r * in[i].pitch;
-        const int lead = static_cast<int>(reinterpret_cast<uint64_t>(far) & 15ull);
-        const int size = static_cast<int>(sizeof(T));
-        Row<T> v;
-        v.near = reinterpret_cast<const T *>(own + (slot * Streams + i) * slot_bytes + lead);
-        v.far = reinterpret_cast<const T *>(far);
-        v.head = lead ? (16 - lead) / size : 0;
-        v.tail = ((lead + row_bytes) / 16 * 16 - lead) / size; // at or before `head` when no granule is whole
-        return v;
+        const int lead = static_cast<int>(reinterpret_cast<uint64_t>(in[i].base + r * in[i].pitch) & 15ull);
+        return Row<T>{reinterpret_cast<const T *>(own + (slot * Streams + i) * slot_bytes + lead), lead};
     }
     // Past a barrier of the group after its last read of the slot.
     __device__ __forceinline__ void next()
@@ -441,6 +549,43 @@ struct Ring {
                 phase ^= 1u;
             }
         }
+    }
+};
+
+// The elements of unaligned rows in granules that are not wholly the row's, at
+// most seven at each end.  Eight lanes of a group's first warp hold each end
+// of each matrix's row, loaded a row before it is written into its slot, which
+// is a row before it is read: no row waits for them.
+template <class T, int Streams>
+struct Edges {
+    static_assert(16 * Streams <= 32, "a warp holds a row's edges");
+    T value{};
+    int at = -1; // its byte in the slot, if this lane holds one
+
+    __device__ __forceinline__ void load(const Ring<Streams> &ring, const Group &g, long long r)
+    {
+        at = -1;
+        const int i = g.lane / 16;
+        if (g.warp != 0 || i >= Streams || r >= ring.rows)
+            return;
+        const int size = static_cast<int>(sizeof(T)), cols = ring.row_bytes / size;
+        const Stream in = i == 0 ? ring.in[0] : ring.in[Streams - 1]; // in registers
+        const T *row = reinterpret_cast<const T *>(in.base + r * in.pitch);
+        const int lead = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u);
+        const int head = lead ? min((16 - lead) / size, cols) : 0;
+        const int tail = max(((lead + ring.row_bytes) / 16 * 16 - lead) / size, head);
+        const int j = g.lane % 8 + (g.lane & 8 ? tail : 0);
+        if (j < (g.lane & 8 ? cols : head)) {
+            value = row[j];
+            at = i * ring.slot_bytes + lead + j * size;
+        }
+    }
+    // Into the group's slot k, which nobody reads any more.
+    __device__ __forceinline__ void place(const Ring<Streams> &ring, uint8_t *own, int k) const
+    {
+        if (at >= 0)
+            *reinterpret_cast<T *>(own + k * Streams * ring.slot_bytes + at) = value;
+        __syncwarp();
     }
 };
 

@@ -364,8 +364,8 @@ def test_refusals_on_device():
 
 
 # Enough rows that every CTA's groups take several in turn: the rows come
-# through shared memory, whole vectors, rows without a rest, or element by
-# element where pitch or base is not 16-byte aligned.
+# through shared memory, as whole vectors, as rows without a rest, or shifted
+# where pitch or base is not 16-byte aligned.
 MANY = [
     # rows, cols, dtype, weight dtype, pad, offset
     (5200, 512, "bf16", "bf16", 0, 0), (9000, 264, "f32", "f32", 0, 0), (4000, 1024, "bf16", "f32", 0, 0),
@@ -421,4 +421,62 @@ def test_a_wait_that_runs_out_is_reported():
         assert status == 6 and detail & 0xFF == 8
     assert torch.equal(pg.layer_norm(x, w), want)
     assert all(torch.equal(a, b) for a, b in zip(pg.layer_norm_backward(x, x, mean, rstd, w), want_b))
+    assert pg.device_status() == (0, 0)
+
+
+# Enough rows for the ring, at pitches that bring every alignment of a row's
+# start, and rows that end inside a vector: 1 to 8 groups of threads a CTA.
+UNALIGNED = [
+    # rows, cols, dtype, weight dtype, pad of x, offset of x, pad and offset of the output
+    (9000, 1, "bf16", "f32", 0, 1, 0, 0), (9000, 2, "f32", "f32", 1, 0, 2, 3), (9000, 7, "bf16", "bf16", 2, 3, 0, 0),
+    (9000, 8, "bf16", "f32", 1, 0, 0, 0), (9000, 9, "bf16", "f32", 0, 0, 4, 5), (9000, 15, "f32", "f32", 0, 1, 1, 2),
+    (9000, 250, "bf16", "bf16", 3, 0, 0, 1), (9000, 257, "bf16", "f32", 0, 0, 0, 0),
+    (5200, 513, "bf16", "bf16", 0, 7, 3, 0), (5200, 520, "f32", "f32", 3, 0, 0, 0),
+    (5200, 1000, "bf16", "f32", 3, 0, 0, 0), (5200, 1000, "f32", "bf16", 1, 2, 5, 1),
+    (1700, 2500, "bf16", "f32", 0, 0, 0, 0), (1700, 2498, "f32", "f32", 0, 0, 1, 0),
+    (1300, 4095, "bf16", "bf16", 2, 0, 0, 0), (1300, 4099, "f32", "f32", 2, 0, 0, 0),
+    (700, 8191, "bf16", "f32", 1, 0, 0, 3), (700, 8192, "bf16", "f32", 3, 0, 0, 0),
+    (700, 8190, "f32", "f32", 0, 1, 1, 0), (400, 12289, "bf16", "f32", 0, 0, 2, 0),
+    (400, 9001, "f32", "f32", 0, 0, 0, 0), (400, 16383, "bf16", "bf16", 0, 5, 0, 0),
+]
+
+
+def _guarded(rows, cols, dtype, pad, offset):
+    """An output amid guards: the view, and a check that nothing around it was written."""
+    import torch
+    buf = torch.full((offset + rows * (cols + pad) + 16,), 7.0, dtype=_torch_dtype(dtype), device="cuda")
+    view = buf[offset:offset + rows * (cols + pad)].view(rows, cols + pad)
+
+    def check():
+        assert (buf[:offset] == 7.0).all() and (view[:, cols:] == 7.0).all() and (buf[-16:] == 7.0).all()
+
+    return view[:, :cols], check
+
+
+@pytest.mark.parametrize("rows,cols,dtype,wdtype,pad,offset,out_pad,out_offset", UNALIGNED)
+def test_unaligned_rows(rows, cols, dtype, wdtype, pad, offset, out_pad, out_offset):
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    x, x64, _ = _make(rows, cols, dtype, pad, seed=rows + 3 * cols, offset=offset, scale=1.2, shift=0.6)
+    w, w64 = _vec(cols, wdtype, 5, 1.0)
+    b, b64 = _vec(cols, wdtype, 6, 0.0)
+    out, check = _guarded(rows, cols, dtype, out_pad, out_offset)
+    y, mean, rstd = pg.layer_norm(x, w, b, out, eps=EPS, stats=True)
+    check()
+    want, m64, r64, e_y, e_m, e_r = _forward_bounds(x64, w64, b64, dtype)
+    _close(y.double().cpu().numpy(), want, e_y, "y")
+    _close(mean.double().cpu().numpy(), m64, e_m, "mean")
+    _close(rstd.double().cpu().numpy(), r64, e_r, "rstd")
+    dy, dy64, _ = _make(rows, cols, dtype, 5 - pad, seed=cols, offset=2, scale=0.01)
+    m64, r64 = mean.double().cpu().numpy(), rstd.double().cpu().numpy()
+    want, bound = _backward_bounds(dy64, x64, m64, r64, w64, dtype, wdtype)
+    out, check = _guarded(rows, cols, dtype, out_pad, out_offset)
+    got = pg.layer_norm_backward(dy, x, mean, rstd, w, out)
+    check()
+    for g, ref, e, what in zip(got, want, bound, ("dx", "dweight", "dbias")):
+        _close(g.double().cpu().numpy(), ref, e, what)
+    # In place, on top of rows whose neighbours share granules: the same bits.
+    gx = x.clone(memory_format=torch.preserve_format) if x.is_contiguous() else x
+    assert torch.equal(pg.layer_norm_backward(dy, gx, mean, rstd, w, dy)[0], got[0])
+    assert torch.equal(pg.layer_norm(x, w, b, x, eps=EPS), y)
     assert pg.device_status() == (0, 0)
