@@ -170,7 +170,11 @@ def _call(device, what, fn, *args):
 
 def _workspace(kind, device, handle, nbytes, other):
     """A buffer kept per operator, device and stream, grown as needed: calls
-    on one stream never overlap."""
+    on one stream never overlap.  A captured call gets its own from the
+    graph's memory: the graph outlives what is kept here, and may run beside
+    calls on the stream it was captured from."""
+    if nbytes and _torch.cuda.is_current_stream_capturing():
+        return _torch.empty(nbytes, dtype=_torch.uint8, device=device)
     key = (kind, device.index, handle)
     buf = _workspaces.get(key)
     if buf is None or buf.numel() < nbytes:
@@ -348,8 +352,8 @@ def orthogonalize(G, out=None, *, steps=5, coefficients=COEFFICIENTS, eps=1e-7, 
 
     coefficients: one (a, b, c) for every step, or `steps` of them.  out:
     where the result goes (G itself for an in-place call).  workspace: "auto"
-    keeps one buffer per device and stream, grown as needed; or a uint8 CUDA
-    tensor of at least orthogonalize_workspace() bytes (the C header)."""
+    keeps one buffer per device and stream, grown as needed (a captured call
+    gets its own, in the graph's memory); or a uint8 CUDA tensor of at least orthogonalize_workspace() bytes (the C header)."""
     torch = _load()
     dt = _dtype(G, "G")
     batch, m, n, ldg, g_batch = _matrices(G, "G")

@@ -354,3 +354,36 @@ def test_out_may_be_G_but_not_overlap_it():
         pg.orthogonalize(buf[:64], buf[1:])
     want = pg.orthogonalize(buf[:64])
     assert torch.equal(pg.orthogonalize(buf[:64], buf[:64]), want)
+
+
+def test_a_captured_call_keeps_its_workspace():
+    """What a graph works in is the graph's: not the stream's buffer, which a
+    larger call replaces and whose memory then goes to other tensors."""
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    g = _gradient(300, 500, "decay", 1).bfloat16()
+    x = torch.randn((3000, 1000), device="cuda")
+    w = torch.ones(1000, device="cuda")
+    _, mean, rstd = pg.layer_norm(x, w, stats=True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        want = pg.orthogonalize(g)
+        want_b = pg.layer_norm_backward(x, x, mean, rstd, w)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            captured = pg.orthogonalize(g)
+            captured_b = pg.layer_norm_backward(x, x, mean, rstd, w)
+        pg.orthogonalize(_gradient(700, 1900, "decay", 1).bfloat16())
+        y = torch.randn((3000, 9000), device="cuda")
+        _, m2, r2 = pg.layer_norm(y, stats=True)
+        pg.layer_norm_backward(y, y, m2, r2, torch.ones(9000, device="cuda"))
+        torch.cuda.synchronize()
+        others = [torch.full((k << 18,), 7, dtype=torch.uint8, device="cuda") for k in range(1, 40)]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all((o == 7).all() for o in others)
+        assert torch.equal(captured, want)
+        assert all(torch.equal(a, b) for a, b in zip(captured_b, want_b))
+    _check_status()
