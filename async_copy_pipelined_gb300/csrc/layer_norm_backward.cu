@@ -2,6 +2,13 @@
 // dy and x are read once and dx written once, and each thread sums dweight and
 // dbias of its columns over all its rows in registers.  What remains of those
 // is one partial sum per column and CTA, added up by a second small kernel.
+//
+// Measured on GB300 (bytes of dy, x and dx): 16384 x 4096 bfloat16 88 us, 4.6
+// TB/s; 3000 x 5000 float32 41 us, 4.4 TB/s; 16384 x 4096 float32 138 us, 5.8
+// TB/s.  In bfloat16 the instructions bound it (two of four issue slots a clock
+// with a quarter of the warps, whose registers the column sums fill); DRAM is
+// busy 55 % of the time.  Above 8192 columns a CTA holds one row of 32 elements
+// a thread and reads it twice from shared memory: 4096 x 16384 bfloat16 125 us.
 #include "layer_norm_internal.h"
 
 namespace pg {

@@ -2,6 +2,14 @@
 // once, y written once.  Mean first, then squared differences to it, from the
 // same registers.  With a ring, weight and bias wait in shared memory as
 // float32 from row to row; otherwise they are loaded beside x.
+//
+// Measured on GB300 (bytes of x and y; a device copy of as many bytes runs at
+// 6.1 TB/s): 16384 x 4096 bfloat16 50 us, 5.4 TB/s; 8192 x 8192 bfloat16 57
+// us, 4.7 TB/s; 16384 x 4096 float32 94 us, 5.7 TB/s.  Neither DRAM (56 % of
+// its cycles at 16384 x 4096 bfloat16) nor the schedulers (1.5 of 4
+// instructions a clock) are full: what is left is a row's two reductions in a
+// row, which the few rows at a time that registers allow hide in part.  One
+// row is the launch: 4096 bfloat16 take about 3 us on the device.
 #include "layer_norm_internal.h"
 
 namespace pg {

@@ -31,12 +31,26 @@
 // Measured in float64 arithmetic on spectra from flat to 1e-3 of the largest
 // value (256 .. 1000 rows): the bfloat16 result is off by 1.03 to 1.15 times
 // the error of rounding the exact result; one pair throughout by up to 16
-// times.
+// times.  float32 result, 1000 x 3000 on GB300: 1.7e-7 for equal singular
+// values and 3.3e-6 for log-spaced ones down to 1e-3, where the formula in
+// float32 arithmetic is off by 7.3e-7 and 4.5e-6.  A fifth pair for Q X, x1 of
+// both, changed that by less than a tenth and took 5 % more time.
 //
 // A A is never added to b A: the square is completed,
 //   Q = c (A + (b / 2c) I)^2 + (a - b b / 4c) I,
 // so that the kernel's whole epilogue is a scaling and a diagonal, and reads
 // nothing.  (c = 0: Q = a I + b A straight from X X^T.)
+//
+// What bounds it, on GB300.  Large sides: an SM's shared memory and then the
+// power limit (the 256 x 256 tile, choose_cut()).  4096 x 4096 bfloat16 takes
+// 1.29 ms, 1.56 PFLOP/s of float16 products done; 8192 x 8192 9.64 ms, 1.66
+// PFLOP/s, where a library's bfloat16 product, under the same limit, sustains
+// 1.69.  Middle sides: the 95 GB/s or so at which an SM takes operands in, and
+// too few tiles (1000 x 3000 float32 343 us, 5000 x 1000 266 us).  Below 500
+// or so the chain of fifteen products, each about 7 us of latency: 1.2 until
+// the next kernel starts, 0.7 to the first operands, 1 of MMAs, 2 of exchange
+// between ranks, 2 of epilogue and stores (256 x 256 114 us); sides of at most
+// 128 have a kernel of their own (orthogonalize_small.cu).
 //
 // Scaling.  G is multiplied by a power of two only, which keeps bfloat16
 // entries exact in float16; the rest of 1 / (|G|_F + eps), a factor f in
@@ -77,7 +91,7 @@ constexpr int kMaxPasses = 5;
 // passes' terms are 2^-11 as large and share one.  Error of the float32 result
 // against float64, 1000 x 3000, flat and decaying spectrum: 9.5e-6 and 1.2e-5
 // with four K blocks to an accumulator, 3.1e-6 and 4.2e-6 with one; the same
-// products in float32 arithmetic give 3.7e-6 and 7.0e-6.
+// products in float32 arithmetic give 3.7e-6 and 7.0e-6 (Q X with five pairs).
 
 enum Output { kPlanes, kBf16, kF32 };
 
@@ -370,13 +384,17 @@ __global__ void __launch_bounds__(Tile<MH, BN, S, Split>::kThreads, 1)
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot_ptr;
     grid_launch_next();
-    grid_wait(); // the operands, f, and the buffers this product overwrites
+    // The kernel before, whose results this one reads and whose operands it
+    // overwrites, is waited for by the roles that touch global memory, each at
+    // its first access: what they work out before that (a tile's place and its
+    // K blocks, about 1 us) no longer stands between two products (2048 x 2048
+    // bfloat16: 399 -> 379 us, 256 x 256 129 -> 114).
 
     if (warp == 0) {
         // ------------------------------------------------------- TMA producer
         if (lane == 0) {
             int f = 0;
-            bool ok = true;
+            bool ok = true, waited = false;
             for (int t = first_tile; t < num_tiles && ok; t += tile_step) {
                 const TileAt at = tile_at(t, symmetric, tiles_m, tiles_n);
                 const int row0 = at.i * BM, col0 = at.j * BN;
@@ -396,6 +414,10 @@ __global__ void __launch_bounds__(Tile<MH, BN, S, Split>::kThreads, 1)
                     for (int kb = kb_lo; kb < kb_hi; ++kb, ++f) {
                         if (f == p.withhold)
                             continue; // test hook: this position is never filled
+                        if (!waited) {
+                            grid_wait();
+                            waited = true;
+                        }
                         if (!ring.producer_acquire(f, p.wait_limit_ns)) {
                             record_error(p.status, kErrFamilyOrthogonalize | kErrRoleProducer);
                             ok = false;
@@ -536,6 +558,7 @@ __global__ void __launch_bounds__(Tile<MH, BN, S, Split>::kThreads, 1)
         static_assert(T::kEpiWarps * kLentBufs * kStagingBytes <= S * T::kStageBytes, "the ring has room to lend");
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         int acc = 0; // accumulators taken
+        grid_wait();
         for (int t = first_tile; t < num_tiles; t += tile_step) {
             const TileAt at = tile_at(t, symmetric, tiles_m, tiles_n);
             const float f = p.f[at.b];
