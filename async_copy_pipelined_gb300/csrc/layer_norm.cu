@@ -130,38 +130,37 @@ __global__ void __launch_bounds__(32 * kColumnRows) columns_kernel(const Backwar
     }
 }
 
-// dweight and dbias from the partial sums: 32 columns by 16 parts of threads,
-// blockIdx.y choosing which of the two.  Four loads of a thread in flight.
-constexpr int kFinishRows = 16;
+// dweight and dbias from the partial sums: 32 columns by 32 parts of threads,
+// blockIdx.y choosing which of the two.  Eight loads of a thread in flight, so
+// that the partial sums of 152 CTAs take one latency.
+constexpr int kFinishRows = 32;
 
 __global__ void __launch_bounds__(32 * kFinishRows) finish_kernel(const Backward p)
 {
-    __shared__ float s[kFinishRows][32];
+    __shared__ float s[kFinishRows][33];
     const int j = blockIdx.x * 32 + threadIdx.x;
     const int which = blockIdx.y;
     void *out = which == 0 ? p.dweight : p.dbias;
+    const float *from = p.partial + static_cast<long long>(which) * p.cols + j;
+    const long long pitch = 2ll * p.cols;
     grid_wait();
     if (!out)
         return;
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (j < p.cols) {
-        const float *from = p.partial + static_cast<long long>(which) * p.cols + j;
-        const long long pitch = 2ll * p.cols;
-        for (int k = threadIdx.y; k < p.parts; k += 4 * kFinishRows) {
+    float sum = 0.0f;
+    for (int k = threadIdx.y; k < p.parts && j < p.cols; k += 8 * kFinishRows) {
+        float v[8];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (k + u * kFinishRows < p.parts)
-                    v[u] += from[(k + u * kFinishRows) * pitch];
-        }
+        for (int u = 0; u < 8; ++u)
+            v[u] = k + u * kFinishRows < p.parts ? from[(k + u * kFinishRows) * pitch] : 0.0f;
+        sum += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
     }
-    s[threadIdx.y][threadIdx.x] = (v[0] + v[1]) + (v[2] + v[3]);
+    s[threadIdx.y][threadIdx.x] = sum;
     __syncthreads();
-    if (threadIdx.y == 0 && j < p.cols) {
-        float t = s[0][threadIdx.x];
-        for (int k = 1; k < kFinishRows; ++k)
-            t += s[k][threadIdx.x];
-        store_f32(out, p.weight_bf16, j, t);
-    }
+    // A warp a column.
+    const float t = warp_sum(s[threadIdx.x][threadIdx.y]);
+    const int column = blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && column < p.cols)
+        store_f32(out, p.weight_bf16, column, t);
 }
 
 constexpr long long kAloneElements = 32768;

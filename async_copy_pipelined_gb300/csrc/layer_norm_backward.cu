@@ -3,7 +3,7 @@
 // dbias of its columns over all its rows in registers.  What remains of those
 // is one partial sum per column and CTA, added up by a second small kernel.
 //
-// Measured on GB300 (bytes of dy, x and dx): 16384 x 4096 bfloat16 88 us, 4.6
+// Measured on GB300 (bytes of dy, x and dx): 16384 x 4096 bfloat16 84 us, 4.8
 // TB/s; 3000 x 5000 float32 41 us, 4.4 TB/s; 16384 x 4096 float32 138 us, 5.8
 // TB/s.  In bfloat16 the instructions bound it (two of four issue slots a clock
 // with a quarter of the warps, whose registers the column sums fill); DRAM is
@@ -181,50 +181,105 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) backward_rows_kernel(cons
 
     if (!p.dweight && !p.dbias)
         return;
-    // The groups' sums in group order, through shared memory (the ring's: all
-    // of its rows have been taken); the last group has the CTA's.
-    float *total = reinterpret_cast<float *>(smem); // [2][cols]
-    for (int k = 0; k < shape.groups; ++k) {
-        if (shape.groups > 1)
-            __syncthreads();
-        if (g.index != k)
-            continue;
-        const bool last = k == shape.groups - 1;
+    if constexpr (!kKeep) {
+        // The groups' sums in group order, each group adding to one copy.  At
+        // these lengths a CTA has one group, whose sums go out as they are;
+        // written for any number, because a form for one, and the one below,
+        // leave the loop over the rows fewer registers (4096 x 16384 bfloat16
+        // 125 and 159 us instead of 121; 7456 x 9000 float32 199 instead of
+        // 174).
+        float *total = reinterpret_cast<float *>(smem); // [2][cols]
+        for (int k = 0; k < shape.groups; ++k) {
+            if (shape.groups > 1)
+                __syncthreads();
+            if (g.index != k)
+                continue;
+            const bool last = k == shape.groups - 1;
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            if (!at.has(i / kPiece, i % kPiece))
-                break;
-            const int j = at.column(i / kPiece) + i % kPiece;
-            float lo, hi;
-            split(dw[i / 2], lo, hi);
-            float vw = i & 1 ? hi : lo;
-            split(db[i / 2], lo, hi);
-            float vb = i & 1 ? hi : lo;
-            if (k > 0) {
-                vw += total[j];
-                vb += total[p.cols + j];
-            }
-            if (!last) {
-                total[j] = vw;
-                total[p.cols + j] = vb;
-            } else if (gridDim.x == 1) {
-                if (p.dweight)
-                    store_f32(p.dweight, p.weight_bf16, j, vw);
-                if (p.dbias)
-                    store_f32(p.dbias, p.weight_bf16, j, vb);
-            } else {
-                float *out = p.partial + static_cast<long long>(blockIdx.x) * 2 * p.cols;
-                out[j] = vw;
-                out[p.cols + j] = vb;
+            for (int i = 0; i < E; ++i) {
+                if (!at.has(i / kPiece, i % kPiece))
+                    break;
+                const int j = at.column(i / kPiece) + i % kPiece;
+                float lo, hi;
+                split(dw[i / 2], lo, hi);
+                float vw = i & 1 ? hi : lo;
+                split(db[i / 2], lo, hi);
+                float vb = i & 1 ? hi : lo;
+                if (k > 0) {
+                    vw += total[j];
+                    vb += total[p.cols + j];
+                }
+                if (!last) {
+                    total[j] = vw;
+                    total[p.cols + j] = vb;
+                } else if (gridDim.x == 1) {
+                    if (p.dweight)
+                        store_f32(p.dweight, p.weight_bf16, j, vw);
+                    if (p.dbias)
+                        store_f32(p.dbias, p.weight_bf16, j, vb);
+                } else {
+                    float *out = p.partial + static_cast<long long>(blockIdx.x) * 2 * p.cols;
+                    out[j] = vw;
+                    out[p.cols + j] = vb;
+                }
             }
         }
+        return;
+    }
+    // Every group's sums to shared memory (the ring's: all of its rows have
+    // been taken), added up in group order and written by neighbouring threads.
+    // (One group after the other adding to one copy, and each thread writing
+    // its own columns, took 1000 x 1024 bfloat16 4 us longer.)
+    const int pitch = parameter_floats(p.cols);
+    float *sums = reinterpret_cast<float *>(smem); // [groups][2][pitch]
+    __syncthreads();
+    float *mine = sums + g.index * 2 * pitch;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+        if (!at.has(k))
+            break;
+        const int j = at.column(k);
+        float vw[kPiece], vb[kPiece];
+#pragma unroll
+        for (int e = 0; e < kPiece; ++e) {
+            const int i = k * kPiece + e;
+            float lo, hi;
+            split(dw[i / 2], lo, hi);
+            vw[e] = i & 1 ? hi : lo;
+            split(db[i / 2], lo, hi);
+            vb[e] = i & 1 ? hi : lo;
+        }
+        if constexpr (kPiece == 1) {
+            mine[j] = vw[0];
+            mine[pitch + j] = vb[0];
+        } else {
+#pragma unroll
+            for (int e = 0; e < kPiece; e += 4) {
+                *reinterpret_cast<uint4 *>(mine + j + e) = Vec16<float>::pack(vw + e);
+                *reinterpret_cast<uint4 *>(mine + pitch + j + e) = Vec16<float>::pack(vb + e);
+            }
+        }
+    }
+    __syncthreads();
+    float *out = p.partial + static_cast<long long>(blockIdx.x) * 2 * p.cols;
+    for (int u = threadIdx.x; u < 2 * p.cols; u += blockDim.x) {
+        const int which = u >= p.cols, j = u - which * p.cols;
+        const float *from = sums + which * pitch + j;
+        float v = from[0];
+        for (int k = 1; k < shape.groups; ++k)
+            v += from[k * 2 * pitch];
+        if (gridDim.x > 1)
+            out[u] = v;
+        else if (void *to = which == 0 ? p.dweight : p.dbias)
+            store_f32(to, p.weight_bf16, j, v);
     }
 }
 
 template <class T, int E, Source S>
 static int launch(const Backward &p, const Plan &plan, const Device &d, cudaStream_t s)
 {
-    const int sums = plan.shape.groups > 1 ? 2 * p.cols * 4 : 0; // the groups' column sums
+    const int copies = E <= 16 ? plan.shape.groups : plan.shape.groups > 1 ? 1 : 0;
+    const int sums = copies * 2 * parameter_floats(p.cols) * 4; // the groups' column sums
     static std::atomic<unsigned long long> limit_set[kMaxDevices];
     if (ensure_smem_limit(backward_rows_kernel<T, E, S>, kSmemBytes, d.index, d.ctx, limit_set) != GEMM_OK)
         return GEMM_ERR_CUDA;

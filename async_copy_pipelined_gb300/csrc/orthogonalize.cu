@@ -34,7 +34,8 @@
 // times.  float32 result, 1000 x 3000 on GB300: 1.7e-7 for equal singular
 // values and 3.3e-6 for log-spaced ones down to 1e-3, where the formula in
 // float32 arithmetic is off by 7.3e-7 and 4.5e-6.  A fifth pair for Q X, x1 of
-// both, changed that by less than a tenth and took 5 % more time.
+// both, takes 5 % more time; without it the error stays below 1.4 times that of
+// float32 arithmetic at every size and spectrum tried.
 //
 // A A is never added to b A: the square is completed,
 //   Q = c (A + (b / 2c) I)^2 + (a - b b / 4c) I,
