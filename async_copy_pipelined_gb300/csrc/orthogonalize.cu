@@ -44,10 +44,10 @@
 //
 // What bounds it, on GB300.  Large sides: an SM's shared memory and then the
 // power limit (the 256 x 256 tile, choose_cut()).  4096 x 4096 bfloat16 takes
-// 1.29 ms, 1.56 PFLOP/s of float16 products done; 8192 x 8192 9.64 ms, 1.66
+// 1.28 ms, 1.57 PFLOP/s of float16 products done; 8192 x 8192 9.46 ms, 1.70
 // PFLOP/s, where a library's bfloat16 product, under the same limit, sustains
 // 1.69.  Middle sides: the 95 GB/s or so at which an SM takes operands in, and
-// too few tiles (1000 x 3000 float32 343 us, 5000 x 1000 266 us).  Below 500
+// too few tiles (1000 x 3000 float32 345 us, 5000 x 1000 269 us).  Below 500
 // or so the chain of fifteen products, each about 7 us of latency: 1.2 until
 // the next kernel starts, 0.7 to the first operands, 1 of MMAs, 2 of exchange
 // between ranks, 2 of epilogue and stores (256 x 256 114 us); sides of at most
