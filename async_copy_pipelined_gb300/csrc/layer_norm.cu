@@ -256,8 +256,9 @@ int launch_backward(Backward p, const Device &d, cudaStream_t s)
     // 16 elements leave room for the two column sums of each in registers.
     const int e = p.cols <= 8192 ? 16 : 32;
     // A gradient of few elements goes to one CTA, which needs no second kernel
-    // to add up column sums: 32 x 1024 bfloat16 rows take it 7 us and two
-    // kernels 5 + 3, of which the second launch costs the host more.
+    // to add up column sums.  32 x 1024 bfloat16 rows take it 8.5 us on the
+    // device and two kernels 5.2, but calls of this size wait for the host,
+    // which needs 20 us for one launch and 24 for two.
     // Not where its groups would take many rows in turn (500 x 64: 39 us).
     const int at_once = std::max(1, kBackwardThreads / ((p.cols + 16 * 32 - 1) / (16 * 32) * 32));
     const bool alone = static_cast<long long>(p.rows) * p.cols <= kAloneElements && p.rows <= 8 * at_once;

@@ -8,7 +8,7 @@
 // TB/s.  In bfloat16 the instructions bound it (two of four issue slots a clock
 // with a quarter of the warps, whose registers the column sums fill); DRAM is
 // busy 55 % of the time.  Above 8192 columns a CTA holds one row of 32 elements
-// a thread and reads it twice from shared memory: 4096 x 16384 bfloat16 125 us.
+// a thread and reads it twice from shared memory: 4096 x 16384 bfloat16 122 us.
 #include "layer_norm_internal.h"
 
 namespace pg {

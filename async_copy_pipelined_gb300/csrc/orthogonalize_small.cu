@@ -4,7 +4,7 @@
 // The iteration is that of orthogonalize.cu, bfloat16 results only, for
 // matrices whose shorter side r is at most 128.  There a product takes a
 // microsecond and the rest of a launch, a round through L2 and the wait for the
-// kernel before take seven.  One CTA holds up to 256 columns of X (two
+// kernel before take six.  One CTA holds up to 256 columns of X (two
 // float16 planes, 128 KiB), and A and then Q in two planes (64 KiB); 1, 2, 4
 // or 8 CTAs, a cluster, hold a matrix.  The square and Q X need no exchange:
 // every CTA has all of A.  X X^T is summed over the CTAs' columns, each rank
@@ -20,8 +20,9 @@
 // cluster two exchanges a step.  The tensor cores work for a tenth of it.
 //
 // Measured on GB300, five steps, bfloat16 (microseconds a call; in brackets
-// orthogonalize.cu's kernels): 64 x 64 35, 128 x 128 43 (106), 128 x 256 51,
-// 100 x 512 66, 128 x 1024 72 (130), 2048 x 128 84; 16 of 100 x 300 82.
+// orthogonalize.cu's kernels): 64 x 64 35 (70), 128 x 128 43 (90), 128 x 256 51
+// (94), 100 x 512 66 (107), 128 x 1024 72 to 76 (113), 2048 x 128 84 to 88
+// (117); 16 of 100 x 300 82.
 #include <algorithm>
 
 #include "orthogonalize_internal.h"
