@@ -172,9 +172,11 @@ def _workspace(kind, device, handle, nbytes, other):
     """A buffer kept per operator, device and stream, grown as needed: calls
     on one stream never overlap.  A captured call gets its own from the
     graph's memory: the graph outlives what is kept here, and may run beside
-    calls on the stream it was captured from."""
+    calls on the stream it was captured from.  It is the launch stream's, so
+    that only work ordered behind this call is given the memory again."""
     if nbytes and _torch.cuda.is_current_stream_capturing():
-        return _torch.empty(nbytes, dtype=_torch.uint8, device=device)
+        with _torch.cuda.stream(other):  # None: the current one
+            return _torch.empty(nbytes, dtype=_torch.uint8, device=device)
     key = (kind, device.index, handle)
     buf = _workspaces.get(key)
     if buf is None or buf.numel() < nbytes:

@@ -480,3 +480,27 @@ def test_unaligned_rows(rows, cols, dtype, wdtype, pad, offset, out_pad, out_off
     assert torch.equal(pg.layer_norm_backward(dy, gx, mean, rstd, w, dy)[0], got[0])
     assert torch.equal(pg.layer_norm(x, w, b, x, eps=EPS), y)
     assert pg.device_status() == (0, 0)
+
+
+def test_a_captured_call_on_a_side_stream_keeps_its_workspace():
+    """The launch stream is a branch of the capture: what the capturing stream
+    allocates and writes beside it must not be the memory the branch works in."""
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    x = torch.randn((3000, 1000), device="cuda")
+    w = torch.ones(1000, device="cuda")
+    _, mean, rstd = pg.layer_norm(x, w, stats=True)
+    want = pg.layer_norm_backward(x, x, mean, rstd, w)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = pg.layer_norm_backward(x, x, mean, rstd, w, stream=side)
+        others = [torch.full((k << 17,), 7, dtype=torch.uint8, device="cuda") for k in range(1, 33)]
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(5):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all((o == 7).all() for o in others)
+        assert all(torch.equal(a, b) for a, b in zip(captured, want))
+    assert pg.device_status() == (0, 0)
