@@ -20,9 +20,6 @@ __all__ = ["layer_norm", "layer_norm_backward", "orthogonalize"]
 
 F32, BF16 = 0, 1  # enum gemm_dtype
 
-_workspaces = {}
-
-
 def bind(l):
     I, L, P, F, S = ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p, ctypes.c_float, ctypes.c_size_t
     l.layer_norm.argtypes = [I, I, P, L, I, P, P, I, P, L, P, P, F, P]
@@ -168,21 +165,15 @@ def _call(device, what, fn, *args):
         raise _pg.GemmError(st, what)
 
 
-def _workspace(kind, device, handle, nbytes, other):
-    """A buffer kept per operator, device and stream, grown as needed: calls
-    on one stream never overlap.  A captured call gets its own from the
-    graph's memory: the graph outlives what is kept here, and may run beside
-    calls on the stream it was captured from.  It is the launch stream's, so
-    that only work ordered behind this call is given the memory again."""
-    if nbytes and _torch.cuda.is_current_stream_capturing():
-        with _torch.cuda.stream(other):  # None: the current one
-            return _torch.empty(nbytes, dtype=_torch.uint8, device=device)
-    key = (kind, device.index, handle)
-    buf = _workspaces.get(key)
-    if buf is None or buf.numel() < nbytes:
-        buf = _workspaces[key] = _torch.empty(nbytes, dtype=_torch.uint8, device=device)
-    _record(other, buf)
-    return buf
+def _workspace(device, nbytes, other):
+    """This call's own buffer, from the launch stream's memory (other None:
+    the current stream's).  A call makes several launches, between which
+    another thread's may come on the same stream: calls share no buffer.
+    Released on return, the memory goes only to work ordered behind them."""
+    if other is None:
+        return _torch.empty(nbytes, dtype=_torch.uint8, device=device)
+    with _torch.cuda.stream(other):
+        return _torch.empty(nbytes, dtype=_torch.uint8, device=device)
 
 
 @functools.lru_cache(maxsize=256)
@@ -303,7 +294,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, *, stream=None
         wdt = _dtype(weight, "weight")
         dweight = torch.empty_like(weight)
         dbias = torch.empty_like(weight)
-        ws = _workspace("layer_norm_backward", device, handle, _norm_bytes(device, rows[0], rows[1]), other)
+        ws = _workspace(device, _norm_bytes(device, rows[0], rows[1]), other)
         ws_bytes = ws.numel()
         pdw, pdb, pws = dweight.data_ptr(), dbias.data_ptr(), ws.data_ptr()
     _call(device, "layer_norm_backward", l.layer_norm_backward, rows[0], rows[1], dy.data_ptr(), dy_rows[2],
@@ -354,8 +345,9 @@ def orthogonalize(G, out=None, *, steps=5, coefficients=COEFFICIENTS, eps=1e-7, 
 
     coefficients: one (a, b, c) for every step, or `steps` of them.  out:
     where the result goes (G itself for an in-place call).  workspace: "auto"
-    keeps one buffer per device and stream, grown as needed (a captured call
-    gets its own, in the graph's memory); or a uint8 CUDA tensor of at least orthogonalize_workspace() bytes (the C header)."""
+    allocates one for the call; or a uint8 CUDA tensor of at least
+    orthogonalize_workspace() bytes (the C header), which serves one call at
+    a time."""
     torch = _load()
     dt = _dtype(G, "G")
     batch, m, n, ldg, g_batch = _matrices(G, "G")
@@ -384,7 +376,7 @@ def orthogonalize(G, out=None, *, steps=5, coefficients=COEFFICIENTS, eps=1e-7, 
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError('workspace must be "auto" or a uint8 CUDA tensor')
-        ws = _workspace("orthogonalize", device, handle, need, other)
+        ws = _workspace(device, need, other)
     else:
         ws = workspace
         if ws.device != device:

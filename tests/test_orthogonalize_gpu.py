@@ -387,3 +387,51 @@ def test_a_captured_call_keeps_its_workspace():
         assert torch.equal(captured, want)
         assert all(torch.equal(a, b) for a, b in zip(captured_b, want_b))
     _check_status()
+
+
+def test_two_threads_on_one_stream():
+    """Launches of two threads' calls mix on the stream they share; neither
+    may work in the other's memory."""
+    import threading
+
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    stream = torch.cuda.Stream()
+    work = []
+    for seed, (m, n) in ((1, (300, 500)), (2, (300, 500))):
+        g = _gradient(m, n, "decay", seed).bfloat16()
+        x = torch.randn((3000, 1000), device="cuda")
+        w = torch.randn(1000, device="cuda")
+        _, mean, rstd = pg.layer_norm(x, w, stats=True)
+        work.append((g, x, mean, rstd, w, pg.orthogonalize(g), pg.layer_norm_backward(x, x, mean, rstd, w)))
+    torch.cuda.synchronize()
+    start, wrong = threading.Barrier(2), []
+
+    def run(g, x, mean, rstd, w, want, want_b):
+        with torch.cuda.stream(stream):
+            start.wait()
+            for _ in range(100):
+                got = pg.orthogonalize(g)
+                got_b = pg.layer_norm_backward(x, x, mean, rstd, w)
+                if not (torch.equal(got, want) and all(torch.equal(a, b) for a, b in zip(got_b, want_b))):
+                    wrong.append(threading.get_ident())
+
+    threads = [threading.Thread(target=run, args=a) for a in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    _check_status()
+
+
+def test_workspaces_are_given_back():
+    """What a call works in is free for other tensors afterwards."""
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    g = _gradient(1024, 2048, "flat", 1)
+    pg.orthogonalize(g)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    o = pg.orthogonalize(g[:1000])
+    assert torch.cuda.memory_allocated() - before <= o.numel() * o.element_size() + 1024
