@@ -69,6 +69,14 @@ def _lib():
     return _pg._lib or _pg.lib()
 
 
+def _counts(name, *sizes):
+    """Sizes that the library takes as C ints, of which ctypes would silently
+    keep the lower 32 bits."""
+    for n in sizes:
+        if n > 0x7FFFFFFF:
+            raise ValueError(f"{name} has a size of {n}: at most 2^31 - 1")
+
+
 def _rows(t, name):
     """(rows, cols, pitch) of a tensor seen as rows of its last dimension:
     the rows' elements contiguous, the rows at one common distance."""
@@ -78,8 +86,10 @@ def _rows(t, name):
     cols = shape[-1]
     if cols < 1:
         raise ValueError(f"{name} has empty rows")
+    count = t.numel() // cols
+    _counts(name, count, cols)
     if t.is_contiguous():
-        return t.numel() // cols, cols, cols
+        return count, cols, cols
     stride = t.stride()
     if cols > 1 and stride[-1] != 1:
         raise ValueError(f"{name} must have unit column stride (row-major rows)")
@@ -316,6 +326,7 @@ def _matrices(t, name):
         raise ValueError(f"{name} must be a matrix or a stack of matrices")
     m, n = t.shape[-2:]
     batch = t.shape[0] if t.dim() == 3 else 1
+    _counts(name, batch, m, n)
     if t.numel() == 0:
         return batch, m, n, max(n, 1), max(m * n, 1)
     if n > 1 and t.stride(-1) != 1:

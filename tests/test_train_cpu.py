@@ -107,3 +107,21 @@ def test_orthogonalize_refuses_host_tensors(lib):
     import torch
     with pytest.raises(ValueError, match="CUDA tensors"):
         pg.orthogonalize(torch.ones((4, 8)))
+
+
+@pytest.mark.parametrize("shape", [(2 ** 32 + 5, 8), (2 ** 31, 1), (3, 2 ** 32 + 8), (2 ** 16, 2 ** 16, 4)])
+def test_counts_beyond_a_c_int_are_refused(lib, shape):
+    """What ctypes would cut to its lower 32 bits: 2^32 + 5 rows to 5."""
+    import torch
+    x = torch.empty(shape, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="2\\^31 - 1"):
+        pg.layer_norm(x)
+    with pytest.raises(ValueError, match="2\\^31 - 1"):
+        pg.layer_norm_backward(x, x, x, x)
+
+
+@pytest.mark.parametrize("shape", [(2 ** 32 + 5, 8), (8, 2 ** 32 + 5), (2 ** 32 + 1, 2, 3)])
+def test_sides_beyond_a_c_int_are_refused(lib, shape):
+    import torch
+    with pytest.raises(ValueError, match="2\\^31 - 1"):
+        pg.orthogonalize(torch.empty(shape, device="meta"))
