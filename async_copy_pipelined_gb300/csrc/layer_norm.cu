@@ -174,8 +174,9 @@ int backward_parts(int rows, int sms)
 
 // Elements per thread `e`, rows at a time, and where they come from.  The
 // ring pays once a group has several rows to run ahead over; below that the
-// threads load their own.  `ctas`: how many share the rows.  `full`: there is a variant for rows without a rest.
-Plan spread(int rows, int cols, int e, int max_threads, int streams, int parameters, bool vectors, bool full,
+// threads load their own.  `ctas`: how many share the rows.  `full`: there is
+// a variant for rows without a rest.
+Plan spread(long long rows, int cols, int e, int max_threads, int streams, int parameters, bool vectors, bool full,
             size_t size, const Device &d, int ctas)
 {
     Plan plan = {};
@@ -183,8 +184,8 @@ Plan spread(int rows, int cols, int e, int max_threads, int streams, int paramet
     if (tpr > max_threads)
         return plan;
     plan.elements = e;
-    const int groups = std::max(1, std::min(max_threads / tpr, (rows + ctas - 1) / ctas));
-    const int trips = (rows + groups - 1) / groups;
+    const int groups = std::max(1, static_cast<int>(std::min<long long>(max_threads / tpr, (rows + ctas - 1) / ctas)));
+    const long long trips = (rows + groups - 1) / groups;
     const int row_bytes = cols * static_cast<int>(size);
     // An unaligned row's last piece is read with the granule after it.
     const int slot_bytes = vectors ? row_bytes : (row_bytes + 15 + 15) / 16 * 16 + 16;
@@ -196,7 +197,7 @@ Plan spread(int rows, int cols, int e, int max_threads, int streams, int paramet
                   : !vectors ? kRingShifted
                   : cols == tpr * e && full ? kRingFull : kRingVector;
     plan.shape = Shape{tpr, groups, slots, slot_bytes, d.status, call_wait_limit_ns(), call_withhold()};
-    plan.grid = std::min(trips, ctas);
+    plan.grid = static_cast<int>(std::min<long long>(trips, ctas));
     plan.smem = ring ? fixed + slots * groups * streams * slot_bytes : 0;
     return plan;
 }

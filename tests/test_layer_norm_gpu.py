@@ -504,3 +504,15 @@ def test_a_captured_call_on_a_side_stream_keeps_its_workspace():
         assert all((o == 7).all() for o in others)
         assert all(torch.equal(a, b) for a, b in zip(captured, want))
     assert pg.device_status() == (0, 0)
+
+
+def test_as_many_rows_as_an_int_counts():
+    """2^31 - 1 rows of one element, each its own mean: y is the bias."""
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    rows = 2 ** 31 - 1
+    x = torch.full((rows, 1), 5.0, dtype=torch.bfloat16, device="cuda")
+    x[-1] = -2.0
+    y = pg.layer_norm(x, torch.ones(1, device="cuda"), torch.full((1,), 3.0, device="cuda"), x)
+    assert all((part == 3.0).all() for part in y.split(1 << 28))
+    assert pg.device_status() == (0, 0)
