@@ -795,7 +795,7 @@ __global__ void __launch_bounds__(Tile<MH, BN, S, Split>::kThreads, 1)
 struct Input {
     Matrix g;
     float eps;
-    float2 *partial; // [batch][parts]
+    float4 *partial; // [batch][parts]
     int parts;
     float *f; // [batch]
     __half *X; // planes of r x pitch, scaled by kScaleX
@@ -804,40 +804,31 @@ struct Input {
 
 constexpr int kNormThreads = 256;
 
-// The sums of squares, one pair of partial sums per CTA.
+// The sums of squares, one set of partial sums per CTA.
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(const Input p)
 {
-    __shared__ float2 scratch[kNormThreads / 32];
+    __shared__ float4 scratch[kNormThreads / 32];
     const int b = blockIdx.y;
     const unsigned units = static_cast<unsigned>((p.g.n + 7) / 8);
     const unsigned total = units * static_cast<unsigned>(p.g.m);
-    float s = 0.0f, t = 0.0f;
+    Squares sum;
     for (unsigned u = blockIdx.x * kNormThreads + threadIdx.x; u < total; u += gridDim.x * kNormThreads) {
         const unsigned row = u / units;
         float v[8];
         load8(p.g, b * p.g.batch_pitch + row * p.g.ld, static_cast<int>(u - row * units) * 8, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            s = fmaf(v[e], v[e], s);
-            const float d = v[e] * kDown;
-            t = fmaf(d, d, t);
-        }
+        for (int e = 0; e < 8; ++e)
+            sum.add(v[e]);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-        t += __shfl_xor_sync(0xffffffffu, t, o);
-    }
+    sum.add_up_warp();
     if (threadIdx.x % 32 == 0)
-        scratch[threadIdx.x / 32] = make_float2(s, t);
+        scratch[threadIdx.x / 32] = sum.sums();
     __syncthreads();
     if (threadIdx.x == 0) {
-        s = t = 0.0f;
-        for (int w = 0; w < kNormThreads / 32; ++w) {
-            s += scratch[w].x;
-            t += scratch[w].y;
-        }
-        p.partial[static_cast<long long>(b) * p.parts + blockIdx.x] = make_float2(s, t);
+        Squares all;
+        for (int w = 0; w < kNormThreads / 32; ++w)
+            all.add(scratch[w]);
+        p.partial[static_cast<long long>(b) * p.parts + blockIdx.x] = all.sums();
     }
 }
 
@@ -853,20 +844,13 @@ __global__ void __launch_bounds__(kNormThreads) planes_kernel(const Input p)
     grid_launch_next();
     grid_wait();
     if (threadIdx.x < 32) {
-        float s = 0.0f, t = 0.0f;
-        for (int k = threadIdx.x; k < p.parts; k += 32) {
-            const float2 v = p.partial[static_cast<long long>(b) * p.parts + k];
-            s += v.x;
-            t += v.y;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            s += __shfl_xor_sync(0xffffffffu, s, o);
-            t += __shfl_xor_sync(0xffffffffu, t, o);
-        }
+        Squares sum;
+        for (int k = threadIdx.x; k < p.parts; k += 32)
+            sum.add(p.partial[static_cast<long long>(b) * p.parts + k]);
+        sum.add_up_warp();
         if (threadIdx.x == 0) {
             int e;
-            const float f = split_scale(s, t, p.eps, &e);
+            const float f = split_scale(sum, p.eps, &e);
             scale[0] = scalbnf(1.0f, e / 2);
             scale[1] = scalbnf(1.0f, e - e / 2);
             if (blockIdx.x == 0 && blockIdx.y == 0)
@@ -956,7 +940,7 @@ Layout make_layout(int batch, int m, int n, int out_dtype, int sms)
         return here;
     };
     const size_t nb = static_cast<size_t>(batch);
-    l.partial = take(nb * l.parts * sizeof(float2));
+    l.partial = take(nb * l.parts * sizeof(float4));
     l.f = take(nb * 4);
     for (size_t &x : l.x)
         x = take(nb * l.xp * l.r * l.cp * 2);
@@ -1173,7 +1157,7 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
 
     // Norm and the first iterate.  A bfloat16 G is exact in one plane.
     const bool exact_input = call.dtype == GEMM_DTYPE_BF16;
-    const Input in{call.matrix(), call.eps, reinterpret_cast<float2 *>(ws + l.partial), l.parts, f,
+    const Input in{call.matrix(), call.eps, reinterpret_cast<float4 *>(ws + l.partial), l.parts, f,
                    static_cast<__half *>(x[0].base), l.xp, exact_input ? 1 : l.xp, l.cp};
     st = launch(norm_kernel, dim3(l.parts, nb), kNormThreads, 0, false, 1, s, in);
     if (st != GEMM_OK)

@@ -76,24 +76,63 @@ __device__ __forceinline__ void load8(const Matrix &p, long long row_at, int j, 
     }
 }
 
-// Squares are summed of the elements, and of 2^-96 times them for the norm of
-// a G whose squares overflow float32.
+// Sums of squares: of the elements, and of 2^-96 and 2^96 times them, for the
+// norm of a G whose squares overflow float32 or vanish in it.
 constexpr float kDown = 1.26217744835361889e-29f; // 2^-96
+constexpr float kUp = 7.92281625142643376e28f;    // 2^96
 
-// From the two sums: f and the power of two e with 2^e f = kScaleX / (|G|_F +
+struct Squares {
+    float plain = 0.0f;
+    unsigned long long scaled = 0ull; // down, up
+
+    __device__ __forceinline__ void add(float v)
+    {
+        plain = fmaf(v, v, plain);
+        const unsigned long long d = mul2(pair(v, v), pair(kDown, kUp));
+        scaled = fma2(d, d, scaled);
+    }
+    __device__ __forceinline__ void add(const float4 &v)
+    {
+        plain += v.x;
+        scaled = add2(scaled, pair(v.y, v.z));
+    }
+    __device__ __forceinline__ void add_up_warp()
+    {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            plain += __shfl_xor_sync(0xffffffffu, plain, o);
+            scaled = add2(scaled, __shfl_xor_sync(0xffffffffu, scaled, o));
+        }
+    }
+    __device__ __forceinline__ float4 sums() const
+    {
+        float down, up;
+        split(scaled, down, up);
+        return make_float4(plain, down, up, 0.0f);
+    }
+};
+
+// Below this sum what vanished of the squares can show; their like in 2^96
+// times the elements stay below 2^122.
+constexpr float kSmallSum = 8.47032947254300339e-22f; // 2^-70
+
+// From the sums: f and the power of two e with 2^e f = kScaleX / (|G|_F +
 // eps), f in [1, 2).  An infinite or NaN norm makes f, and so every element
 // that comes of it, NaN.
-__device__ __forceinline__ float split_scale(float s, float t, float eps, int *e)
+__device__ __forceinline__ float split_scale(const Squares &squares, float eps, int *e)
 {
     const float inf = __int_as_float(0x7f800000);
-    const bool big = !(s < inf);
-    const float norm = big ? sqrtf(t) : sqrtf(s);
-    const float inv = big ? 1.0f / (norm + eps * kDown) : 1.0f / (norm + eps);
+    const float4 s = squares.sums();
+    const bool big = !(s.x < inf);
+    const bool small = s.x < kSmallSum && eps * kUp < inf;
+    const float unit = big ? kDown : small ? kUp : 1.0f; // `norm` is so many times |G|_F
+    const float norm = sqrtf(big ? s.y : small ? s.z : s.x);
+    const float inv = 1.0f / (norm + eps * unit);
     *e = 0;
     if (!(norm < inf && inv < inf))
         return __int_as_float(0x7fc00000);
     const int k = ilogbf(inv);
-    *e = k + (big ? -96 : 0) + 14; // kScaleX
+    *e = k + (big ? -96 : small ? 96 : 0) + 14; // kScaleX
     return scalbnf(inv, -k);
 }
 

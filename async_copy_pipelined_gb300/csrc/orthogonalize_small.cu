@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[3];
     __shared__ uint32_t tmem_slot;
-    __shared__ float2 warp_sums[kSmallThreads / 32];
-    __shared__ float2 rank_sums[kMaxRanks];
+    __shared__ float4 warp_sums[kSmallThreads / 32];
+    __shared__ float4 rank_sums[kMaxRanks];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = align_smem(raw, 1024); // the same offset in every CTA of the cluster
     const uint32_t done = smem_u32(&bars[0]), drained = smem_u32(&bars[1]), arrived = smem_u32(&bars[2]);
@@ -172,43 +172,33 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
             }
         }
     };
-    float s = 0.0f, t = 0.0f;
+    Squares sum;
     visit([&](const float (&v)[8], int, int) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            s = fmaf(v[e], v[e], s);
-            const float d = v[e] * kDown;
-            t = fmaf(d, d, t);
-        }
+        for (int e = 0; e < 8; ++e)
+            sum.add(v[e]);
     });
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-        t += __shfl_xor_sync(0xffffffffu, t, o);
-    }
+    sum.add_up_warp();
     if (lane == 0)
-        warp_sums[warp] = make_float2(s, t);
+        warp_sums[warp] = sum.sums();
     __syncthreads();
     if (threadIdx.x < p.ranks) { // this CTA's sums to rank threadIdx.x
-        s = t = 0.0f;
-        for (int w = 0; w < kSmallThreads / 32; ++w) {
-            s += warp_sums[w].x;
-            t += warp_sums[w].y;
-        }
-        const uint32_t slot = smem_u32(&rank_sums[rank]);
+        Squares cta;
+        for (int w = 0; w < kSmallThreads / 32; ++w)
+            cta.add(warp_sums[w]);
+        const float4 q = cta.sums();
         if (p.ranks > 1)
-            st_cluster_v2(map_to_cta(slot, threadIdx.x), __float_as_uint(s), __float_as_uint(t));
+            st_cluster_v4(map_to_cta(smem_u32(&rank_sums[rank]), threadIdx.x), __float_as_uint(q.x),
+                          __float_as_uint(q.y), __float_as_uint(q.z), __float_as_uint(q.w));
         else
-            rank_sums[0] = make_float2(s, t);
+            rank_sums[0] = q;
     }
     sync();
-    s = t = 0.0f;
-    for (int k = 0; k < p.ranks; ++k) {
-        s += rank_sums[k].x;
-        t += rank_sums[k].y;
-    }
+    Squares all;
+    for (int k = 0; k < p.ranks; ++k)
+        all.add(rank_sums[k]);
     int e2;
-    const float f = split_scale(s, t, p.eps, &e2);
+    const float f = split_scale(all, p.eps, &e2);
     const float s0 = scalbnf(1.0f, e2 / 2), s1 = scalbnf(1.0f, e2 - e2 / 2);
     const bool exact = p.g.bf16 != 0; // one plane holds a bfloat16 G
     visit([&](const float (&v)[8], int i, int j) {

@@ -287,11 +287,6 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_
                  : "memory");
 }
 
-__device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_t b)
-{
-    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};\n" ::"r"(addr), "r"(a), "r"(b) : "memory");
-}
-
 // Bulk copy of this CTA's shared memory at `src` to an address of another CTA
 // of the cluster, completing on a barrier of that one (both from map_to_cta);
 // 16-byte aligned, a multiple of 16 bytes.

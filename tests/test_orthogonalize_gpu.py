@@ -435,3 +435,17 @@ def test_workspaces_are_given_back():
     before = torch.cuda.memory_allocated()
     o = pg.orthogonalize(g[:1000])
     assert torch.cuda.memory_allocated() - before <= o.numel() * o.element_size() + 1024
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n", [(96, 160), (130, 500), (300, 140)])
+@pytest.mark.parametrize("scale,eps", [(1e-38, 0.0), (1e-36, 1e-37), (1e-30, 1e-28), (1e-30, 0.0), (1e-23, 1e-24),
+                                       (1e-20, 0.0), (1e-12, 1e-12), (1e-10, 1e-10)])
+def test_a_small_norm(dtype, m, n, scale, eps):
+    """Squares that vanish in float32, in part or all of them, still make the
+    norm, down to elements that are float32's last denormals."""
+    import async_copy_pipelined_gb300 as pg
+    g = (_gradient(m, n, "flat", 11, scale=1.0) * scale).to(_torch_dtype(dtype))
+    assert _rel(pg.orthogonalize(g, eps=eps), _exact(g, eps=np.float32(eps).item())) <= _tol(dtype, g)
+    assert (pg.orthogonalize(g * 0, eps=max(eps, 1e-40)) == 0).all()
+    _check_status()
