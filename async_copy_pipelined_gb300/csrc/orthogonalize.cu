@@ -54,8 +54,8 @@
 // 128 have a kernel of their own (orthogonalize_small.cu).
 //
 // Scaling.  G is multiplied by a power of two only, which keeps bfloat16
-// entries exact in float16; the rest of 1 / (|G|_F + eps), a factor f in
-// [1, 2), goes into the first step's epilogues in float32.
+// entries exact in float16; the rest of 1 / (|G|_F + eps) goes into the
+// epilogues in float32, of the first step unless eps dwarfs |G|_F (Factors).
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -121,8 +121,8 @@ struct Product {
     int ranks; // CTAs that share a tile's K blocks
     int fine; // Fine: accumulators of the last pass; the passes before it have one
     float alpha, diag;
-    int alpha_power, diag_power; // of f
-    const float *f;              // one per matrix
+    int alpha_g, alpha_rho, diag_rho; // powers of this step's Factors
+    const Factors *f; // of matrix b at f[b * kFactors]
     int output;                  // Output
     int planes;                  // kPlanes: how many to write
     int planes_pitch;            // kPlanes: planes per matrix of the batch
@@ -562,12 +562,14 @@ __global__ void __launch_bounds__(Tile<MH, BN, S, Split>::kThreads, 1)
         grid_wait();
         for (int t = first_tile; t < num_tiles; t += tile_step) {
             const TileAt at = tile_at(t, symmetric, tiles_m, tiles_n);
-            const float f = p.f[at.b];
+            const Factors f = p.f[at.b * kFactors];
             float alpha = p.alpha, diag = p.diag;
-            for (int e = 0; e < p.alpha_power; ++e)
-                alpha *= f;
-            for (int e = 0; e < p.diag_power; ++e)
-                diag *= f;
+            for (int e = 0; e < p.alpha_g; ++e)
+                alpha *= f.g;
+            if (p.alpha_rho)
+                alpha *= f.rho;
+            if (p.diag_rho)
+                diag *= f.rho;
             const int row0 = at.i * BM + half * kUmmaM + quarter * 32;
             const int row = row0 + lane;
             const bool mirrored = symmetric && at.i != at.j;
@@ -797,7 +799,9 @@ struct Input {
     float eps;
     float4 *partial; // [batch][parts]
     int parts;
-    float *f; // [batch]
+    Factors *f; // [batch][kFactors]
+    int steps;
+    Slow slow[kMaxSteps];
     __half *X; // planes of r x pitch, scaled by kScaleX
     int planes, write_planes, pitch;
 };
@@ -833,12 +837,11 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const Input p)
 }
 
 // X's planes from a 64 x 64 piece of G (transposed where G is tall), after
-// the norm from the partial sums: G times the power of two in
-// 1 / (|G|_F + eps), and f, the rest of it.
+// the norm from the partial sums, and the factors of every step.
 template <bool Tall>
 __global__ void __launch_bounds__(kNormThreads) planes_kernel(const Input p)
 {
-    __shared__ float scale[2];
+    __shared__ float scale[3];
     __shared__ float piece[Tall ? 64 : 1][65];
     const int b = blockIdx.z;
     grid_launch_next();
@@ -850,14 +853,19 @@ __global__ void __launch_bounds__(kNormThreads) planes_kernel(const Input p)
         sum.add_up_warp();
         if (threadIdx.x == 0) {
             int e;
-            const float f = split_scale(sum, p.eps, &e);
-            scale[0] = scalbnf(1.0f, e / 2);
-            scale[1] = scalbnf(1.0f, e - e / 2);
-            if (blockIdx.x == 0 && blockIdx.y == 0)
-                p.f[b] = f;
+            scale[2] = split_scale(sum, p.eps, &e);
+            scale[0] = power_of_two(e / 2);
+            scale[1] = power_of_two(e - e / 2);
         }
     }
     __syncthreads();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == kNormThreads - 1) {
+        float g = scale[2];
+        Factors *f = p.f + b * kFactors;
+        for (int k = 0; k < p.steps; ++k)
+            f[k] = step_factors(g, p.slow[k]);
+        f[p.steps] = Factors{g, 1.0f}; // of the result
+    }
     const float s0 = scale[0], s1 = scale[1];
     const int r = Tall ? p.g.n : p.g.m, c = Tall ? p.g.m : p.g.n;
     const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
@@ -941,7 +949,7 @@ Layout make_layout(int batch, int m, int n, int out_dtype, int sms)
     };
     const size_t nb = static_cast<size_t>(batch);
     l.partial = take(nb * l.parts * sizeof(float4));
-    l.f = take(nb * 4);
+    l.f = take(nb * kFactors * sizeof(Factors));
     for (size_t &x : l.x)
         x = take(nb * l.xp * l.r * l.cp * 2);
     l.a = take(nb * l.ap * l.r * l.rp * 2);
@@ -1095,7 +1103,7 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
     const Planes a{ws + l.a, l.r, l.r, l.rp, nb * l.ap}, q{ws + l.q, l.r, l.r, l.rp, nb * l.ap};
     const Planes a_diag{ws + l.a_diag, l.r, kDiagBlock, kDiagBlock, nb};
     const Planes q_diag{ws + l.q_diag, l.r, kDiagBlock, kDiagBlock, nb};
-    float *f = reinterpret_cast<float *>(ws + l.f);
+    Factors *f = reinterpret_cast<Factors *>(ws + l.f);
 
     // The cuts of X X^T, of the square and of Q X, for the K blocks of the
     // passes a middle step makes.
@@ -1157,8 +1165,10 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
 
     // Norm and the first iterate.  A bfloat16 G is exact in one plane.
     const bool exact_input = call.dtype == GEMM_DTYPE_BF16;
-    const Input in{call.matrix(), call.eps, reinterpret_cast<float4 *>(ws + l.partial), l.parts, f,
-                   static_cast<__half *>(x[0].base), l.xp, exact_input ? 1 : l.xp, l.cp};
+    Input in{call.matrix(), call.eps, reinterpret_cast<float4 *>(ws + l.partial), l.parts, f, call.steps, {},
+             static_cast<__half *>(x[0].base), l.xp, exact_input ? 1 : l.xp, l.cp};
+    for (int k = 0; k < call.steps; ++k)
+        in.slow[k] = slow_step(call.coefficients + 3 * k);
     st = launch(norm_kernel, dim3(l.parts, nb), kNormThreads, 0, false, 1, s, in);
     if (st != GEMM_OK)
         return st;
@@ -1170,7 +1180,6 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
 
     Product base = {};
     base.batch = nb;
-    base.f = f;
     base.status = status;
     base.wait_limit_ns = call_wait_limit_ns();
     base.withhold = call_withhold();
@@ -1181,6 +1190,7 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
         const bool first = step == 0, last = step == call.steps - 1;
         const bool one_plane = first && exact_input; // X has no more than that
         const int cur = step & 1;
+        base.f = f + step;
         auto add = [](Product &p, int left, int right, Range range) {
             p.pass[p.passes++] = Pass{static_cast<signed char>(left), static_cast<signed char>(right),
                                       static_cast<signed char>(range)};
@@ -1203,12 +1213,12 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
         if (cc != 0.0f) {
             p.alpha = kScaleA / (kScaleX * kScaleX);
             p.diag = kScaleA * (cb / (2.0f * cc));
-            p.alpha_power = first ? 2 : 0;
+            p.alpha_g = 2;
         } else {
             p.alpha = kScaleQ * cb / (kScaleX * kScaleX);
             p.diag = kScaleQ * ca;
-            p.alpha_power = first ? 3 : 0;
-            p.diag_power = first ? 1 : 0;
+            p.alpha_g = 2;
+            p.alpha_rho = p.diag_rho = 1;
         }
         maps.left = maps.right = x_load[cur];
         set_stores(maps, cc != 0.0f ? to_a : to_q);
@@ -1234,7 +1244,7 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
             p.diag_plane = 1;
             p.alpha = kScaleQ * cc / (kScaleA * kScaleA);
             p.diag = kScaleQ * static_cast<float>(ca - static_cast<double>(cb) * cb / (4.0 * cc));
-            p.alpha_power = p.diag_power = first ? 1 : 0;
+            p.alpha_rho = p.diag_rho = 1;
             maps.left = maps.right = a_load;
             maps.left_diag = maps.right_diag = a_diag_load;
             set_stores(maps, to_q);
@@ -1268,6 +1278,8 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
         if (last) {
             p.output = wide_result ? kF32 : kBf16;
             p.alpha = 1.0f / (kScaleQ * kScaleX);
+            p.f = f + call.steps;
+            p.alpha_g = 1;
             p.transposed = tall;
             p.out_tma = out_tma;
             p.out = call.out;
@@ -1289,7 +1301,7 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
 
 // Whether the iteration stays where the planes can hold it: from singular
 // values in [0, 1], every step's values within [0, 2] and Q within 15
-// (30 with the first step's f below 2).
+// (30 with g below 2).
 int check_coefficients(const float *coefficients, int steps)
 {
     double top = 1.0;
@@ -1317,7 +1329,6 @@ int check_coefficients(const float *coefficients, int steps)
 
 bool valid_dtype(int d) { return d == GEMM_DTYPE_F32 || d == GEMM_DTYPE_BF16; }
 
-constexpr int kMaxSteps = 32;
 constexpr int kMaxSide = 1 << 20;
 constexpr long long kMaxElements = 0x7fffffffll;
 constexpr int kMaxBatch = 65535;

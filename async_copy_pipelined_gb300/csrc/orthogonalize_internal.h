@@ -3,6 +3,7 @@
 // (orthogonalize.cu) hands it on.
 #pragma once
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -81,6 +82,9 @@ __device__ __forceinline__ void load8(const Matrix &p, long long row_at, int j, 
 constexpr float kDown = 1.26217744835361889e-29f; // 2^-96
 constexpr float kUp = 7.92281625142643376e28f;    // 2^96
 
+// 2^k for |k| below 127.
+__device__ __forceinline__ float power_of_two(int k) { return __int_as_float((127 + k) << 23); }
+
 struct Squares {
     float plain = 0.0f;
     unsigned long long scaled = 0ull; // down, up
@@ -116,25 +120,62 @@ struct Squares {
 // times the elements stay below 2^122.
 constexpr float kSmallSum = 8.47032947254300339e-22f; // 2^-70
 
-// From the sums: f and the power of two e with 2^e f = kScaleX / (|G|_F +
-// eps), f in [1, 2).  An infinite or NaN norm makes f, and so every element
-// that comes of it, NaN.
+// The planes hold X up to a factor, X = g Y: Y is G times a power of two that
+// depends on |G|_F alone, so that its norm is in (1/2, 1] however eps compares
+// with |G|_F and float16 keeps its bits; g = 2^-e / (|G|_F + eps), at most 2,
+// goes into the products' epilogues in float32.
+//
+// From the sums: g, and in *e the power of two with kScaleX.  An infinite or
+// NaN norm makes g, and so every element that comes of it, NaN.
 __device__ __forceinline__ float split_scale(const Squares &squares, float eps, int *e)
 {
-    const float inf = __int_as_float(0x7f800000);
+    const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fc00000);
     const float4 s = squares.sums();
-    const bool big = !(s.x < inf);
-    const bool small = s.x < kSmallSum && eps * kUp < inf;
+    const bool big = !(s.x < inf), small = s.x < kSmallSum;
     const float unit = big ? kDown : small ? kUp : 1.0f; // `norm` is so many times |G|_F
     const float norm = sqrtf(big ? s.y : small ? s.z : s.x);
-    const float inv = 1.0f / (norm + eps * unit);
     *e = 0;
-    if (!(norm < inf && inv < inf))
-        return __int_as_float(0x7fc00000);
-    const int k = ilogbf(inv);
+    if (!(norm < inf))
+        return nan;
+    if (norm == 0.0f)
+        return eps > 0.0f ? 1.0f : nan;
+    // norm is a normal number between 2^-54 and 2^64: 2^k norm in (1/2, 1].
+    const int bits = __float_as_int(norm), k = 127 - (bits >> 23) - ((bits & 0x7fffff) != 0 ? 1 : 0);
     *e = k + (big ? -96 : small ? 96 : 0) + 14; // kScaleX
-    return scalbnf(inv, -k);
+    // eps unit may be infinite: then g is zero, and |G|_F / eps below 2^-67.
+    return power_of_two(-k) / (norm + eps * unit);
 }
+
+// What a step's epilogues multiply by: A = X X^T by g g, Q by rho, so that the
+// next X is (g / rho) (rho Q) Y and Y becomes rho Q Y.  As soon as g is not
+// small Q takes all of it, and from then on X is Y.  Until then X is so small
+// that Q is nearly a I, and rho keeps Y from growing.
+struct alignas(8) Factors {
+    float g, rho;
+};
+constexpr float kSmallG = 0.0625f;
+
+// How large Q can be while singular values are at most kSmallG, and 1 / that.
+struct Slow {
+    float most, inverse;
+};
+inline Slow slow_step(const float *coefficients)
+{
+    const float most = std::max(1.0f, std::fabs(coefficients[0]) + std::fabs(coefficients[1]) * 0x1p-8f +
+                                          std::fabs(coefficients[2]) * 0x1p-16f);
+    return Slow{most, 1.0f / most};
+}
+// This step's factors; g becomes the next step's.
+__device__ __forceinline__ Factors step_factors(float &g, const Slow &slow)
+{
+    const bool small = g < kSmallG;
+    const Factors f{g, small ? slow.inverse : g};
+    g = small ? g * slow.most : 1.0f;
+    return f;
+}
+
+constexpr int kMaxSteps = 32;
+constexpr int kFactors = kMaxSteps + 1; // per matrix: each step's, and the result's
 
 // `overlap`: the kernel may start while the one before it ends (it calls
 // grid_wait()); `cluster`: CTAs per cluster.

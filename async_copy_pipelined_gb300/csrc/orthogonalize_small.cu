@@ -35,7 +35,6 @@ constexpr int kSmallRows = 128;
 constexpr int kSlab = 256;     // columns of X that a CTA holds
 constexpr int kMaxRanks = 8;
 constexpr int kSmallThreads = 512;
-constexpr int kSmallSteps = 32;
 constexpr uint32_t kColumnBlock = kSmallRows * 128; // 64 columns: 16 KiB
 constexpr uint32_t kUnit = 32 * 32 * 4;             // a warp's share of a 128 x 128 sum
 constexpr uint32_t kStrip = 32 * 128;               // 32 rows of a column block: one piece of a plane
@@ -63,7 +62,8 @@ struct Small {
     unsigned int *status;
     unsigned long long wait_limit_ns;
     int withhold;
-    float coefficients[3 * kSmallSteps];
+    float coefficients[3 * kMaxSteps];
+    Slow slow[kMaxSteps];
 };
 
 constexpr uint32_t instruction(int n, bool right_mn)
@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     for (int k = 0; k < p.ranks; ++k)
         all.add(rank_sums[k]);
     int e2;
-    const float f = split_scale(all, p.eps, &e2);
-    const float s0 = scalbnf(1.0f, e2 / 2), s1 = scalbnf(1.0f, e2 - e2 / 2);
+    float g = split_scale(all, p.eps, &e2);
+    const float s0 = power_of_two(e2 / 2), s1 = power_of_two(e2 - e2 / 2);
     const bool exact = p.g.bf16 != 0; // one plane holds a bfloat16 G
     visit([&](const float (&v)[8], int i, int j) {
         float x[8];
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
         const float ca = p.coefficients[3 * step], cb = p.coefficients[3 * step + 1],
                     cc = p.coefficients[3 * step + 2];
         const bool first = step == 0, last = step == p.steps - 1;
-        const float fs = first ? f : 1.0f;
+        const Factors f = step_factors(g, p.slow[step]);
         unsigned long long v[16];
         uint32_t w[16];
 
@@ -355,9 +355,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
                 mbar_arrive_expect_tx(arrived, static_cast<uint32_t>(8 - 8 / p.ranks) * 2u * kStrip);
         }
         if (cc != 0.0f)
-            scale(v, kScaleA / (kScaleX * kScaleX) * fs * fs, kScaleA * (cb / (2.0f * cc)));
+            scale(v, kScaleA / (kScaleX * kScaleX) * f.g * f.g, kScaleA * (cb / (2.0f * cc)));
         else
-            scale(v, kScaleQ * cb / (kScaleX * kScaleX) * fs * fs * fs, kScaleQ * ca * fs);
+            scale(v, kScaleQ * cb / (kScaleX * kScaleX) * f.g * f.g * f.rho, kScaleQ * ca * f.rho);
         const uint32_t row_at = static_cast<uint32_t>(part / 2) * kColumnBlock + static_cast<uint32_t>(row) * 128u;
         if (owner == rank) {
             for (int q = 0; q < 2; ++q) {
@@ -393,8 +393,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
                 square_pass(on, base + kA0, base + kA0, k_blocks, false);
             });
             read(part * 32, v);
-            scale(v, kScaleQ * cc / (kScaleA * kScaleA) * fs,
-                  kScaleQ * static_cast<float>(ca - static_cast<double>(cb) * cb / (4.0 * cc)) * fs);
+            scale(v, kScaleQ * cc / (kScaleA * kScaleA) * f.rho,
+                  kScaleQ * static_cast<float>(ca - static_cast<double>(cb) * cb / (4.0 * cc)) * f.rho);
             if (p.ranks > 1)
                 cluster_wait(); // before Q replaces the strips this rank has sent
             for (int q = 0; q < 2; ++q) {
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
         });
         for (int k = part; k < 2 * p.blocks; k += 4) { // 32 columns each
             read(kResult + k * 32, v);
-            const float alpha = last ? 1.0f / (kScaleQ * kScaleX) : 1.0f / kScaleQ;
+            const float alpha = last ? 1.0f / (kScaleQ * kScaleX) * g : 1.0f / kScaleQ;
             const unsigned long long a2 = pair(alpha, alpha);
 #pragma unroll
             for (int j = 0; j < 16; ++j)
@@ -520,6 +520,8 @@ int run_small(const Call &call, const Device &d, unsigned int *status, cudaStrea
     p.withhold = call_withhold();
     for (int k = 0; k < 3 * call.steps; ++k)
         p.coefficients[k] = call.coefficients[k];
+    for (int k = 0; k < call.steps; ++k)
+        p.slow[k] = slow_step(call.coefficients + 3 * k);
     static std::atomic<unsigned long long> limit_set[kMaxDevices];
     if (ensure_smem_limit(small_kernel, kSmallSmem, d.index, d.ctx, limit_set) != GEMM_OK)
         return GEMM_ERR_CUDA;

@@ -449,3 +449,29 @@ def test_a_small_norm(dtype, m, n, scale, eps):
     assert _rel(pg.orthogonalize(g, eps=eps), _exact(g, eps=np.float32(eps).item())) <= _tol(dtype, g)
     assert (pg.orthogonalize(g * 0, eps=max(eps, 1e-40)) == 0).all()
     _check_status()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n", [(96, 160), (120, 900), (130, 500), (300, 140), (1000, 700)])
+@pytest.mark.parametrize("scale", [1e-9, 3e-11, 1e-12, 1e-15, 1e-20, 1e-28])
+@pytest.mark.parametrize("steps,coefficients", [(5, TRIPLE), (1, TRIPLE), (9, (1.5, -0.5, 0.0)),
+                                                (12, (1.875, -1.25, 0.375))])
+def test_eps_beyond_the_norm(dtype, m, n, scale, steps, coefficients):
+    """|G|_F far below eps: X starts at |G|_F / eps, and what the result keeps
+    of it is relative to its own size."""
+    import async_copy_pipelined_gb300 as pg
+    g = (_gradient(m, n, "flat", 12, scale=1.0) * scale).to(_torch_dtype(dtype))
+    want = _exact(g, steps, coefficients, eps=np.float32(1e-7).item())
+    assert _rel(pg.orthogonalize(g, steps=steps, coefficients=coefficients), want) <= _tol(dtype, g)
+    _check_status()
+
+
+def test_eps_beyond_the_norm_of_some_matrices():
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    for m, n in ((100, 400), (200, 300)):
+        g = torch.stack([_gradient(m, n, "decay", b, scale=10.0 ** -(4 * b)) for b in range(5)])
+        o = pg.orthogonalize(g)
+        for b in range(5):
+            assert _rel(o[b], _exact(g[b], eps=np.float32(1e-7).item())) <= _tol("f32", g[b])
+            assert torch.equal(o[b], pg.orthogonalize(g[b])) or m > 128  # larger ones may be cut otherwise
