@@ -119,17 +119,41 @@ def _vector(t, name, n, device):
     return t.data_ptr()
 
 
-def _span(t, rows, cols, pitch):
-    first = t.data_ptr()
-    return first, first + ((rows - 1) * pitch + cols) * t.element_size()
+def _share_bytes(a, b):
+    """Whether two stacks of matrices may share a byte.  Each: address, then
+    matrices, rows, columns, row pitch, matrix pitch and element size.  Views
+    of one buffer at the same pitches are told apart by their place within a
+    pitch; what this does not show to be apart counts as shared."""
+    (pa, na, ma, ca, la, ba, ea), (pb, nb, mb, cb, lb, bb, eb) = a, b
+    wide_a, wide_b = ca * ea, cb * eb  # bytes of a row, of a matrix, of all
+    tall_a, tall_b = ((ma - 1) * la) * ea + wide_a, ((mb - 1) * lb) * eb + wide_b
+    if pa + (na - 1) * ba * ea + tall_a <= pb or pb + (nb - 1) * bb * eb + tall_b <= pa:
+        return False
+
+    def apart(pitch, size_a, size_b):
+        at = (pb - pa) % pitch
+        return at >= size_a and at + size_b <= pitch
+
+    # A single row or matrix fits any pitch.
+    if ma == 1 or mb == 1 or la * ea == lb * eb:
+        pitch = la * ea if ma > 1 else lb * eb
+        whole = all(n == 1 or (d * e) % pitch == 0 for n, d, e in ((na, ba, ea), (nb, bb, eb)))
+        if pitch > 0 and whole and apart(pitch, wide_a, wide_b):
+            return False
+    if na == 1 or nb == 1 or ba * ea == bb * eb:
+        pitch = ba * ea if na > 1 else bb * eb
+        if (na > 1 or nb > 1) and pitch > 0 and apart(pitch, tall_a, tall_b):
+            return False
+    return True
 
 
 def _refuse_overlap(out, out_rows, t, t_rows, name, what):
     """An output may be an input itself, row on row, but not overlap it otherwise."""
     if out_rows[0] == 0:
         return
-    a, b = _span(out, *out_rows), _span(t, *t_rows)
-    if a[0] < b[1] and b[0] < a[1] and not (a[0] == b[0] and out_rows == t_rows and out.dtype == t.dtype):
+    if out.data_ptr() == t.data_ptr() and out_rows == t_rows and out.dtype == t.dtype:
+        return
+    if _share_bytes(*((x.data_ptr(), 1, *rows, 0, x.element_size()) for x, rows in ((out, out_rows), (t, t_rows)))):
         raise ValueError(f"{what} overlaps {name} in memory; it may only be {name} itself")
 
 
@@ -337,11 +361,6 @@ def _matrices(t, name):
     return batch, m, n, pitch, t.stride(0) if batch > 1 else pitch * (m - 1) + n
 
 
-def _extent(t, m, n, batch, pitch, matrix_pitch):
-    first = t.data_ptr()
-    return first, first + ((batch - 1) * matrix_pitch + (m - 1) * pitch + n) * t.element_size()
-
-
 def orthogonalize(G, out=None, *, steps=5, coefficients=COEFFICIENTS, eps=1e-7, dtype=None, workspace="auto",
                   stream=None):
     """The orthogonalised form of a weight's update G, by Newton-Schulz products.
@@ -376,8 +395,8 @@ def orthogonalize(G, out=None, *, steps=5, coefficients=COEFFICIENTS, eps=1e-7, 
     odt = _dtype(out, "out")
     _, _, _, ldo, o_batch = _matrices(out, "out")
     if out.numel() and not (out.data_ptr() == G.data_ptr() and odt == dt and (ldo, o_batch) == (ldg, g_batch)):
-        a, b = _extent(out, m, n, batch, ldo, o_batch), _extent(G, m, n, batch, ldg, g_batch)
-        if a[0] < b[1] and b[0] < a[1]:
+        if _share_bytes((out.data_ptr(), batch, m, n, ldo, o_batch, out.element_size()),
+                        (G.data_ptr(), batch, m, n, ldg, g_batch, G.element_size())):
             raise ValueError("out overlaps G in memory; it may only be G itself")
     if batch > 1 and out.numel() and o_batch < ldo * (m - 1) + n:
         raise ValueError("the matrices of out overlap in memory")

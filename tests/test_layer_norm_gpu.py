@@ -516,3 +516,29 @@ def test_as_many_rows_as_an_int_counts():
     y = pg.layer_norm(x, torch.ones(1, device="cuda"), torch.full((1,), 3.0, device="cuda"), x)
     assert all((part == 3.0).all() for part in y.split(1 << 28))
     assert pg.device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols,gap", [(4, 64, 0), (40, 100, 0), (40, 101, 3), (5000, 512, 0), (5000, 333, 1)])
+def test_a_slice_of_the_same_buffer_may_be_the_output(rows, cols, gap, dtype):
+    """Column slices side by side share no byte: x, dy and the output in one
+    buffer, whose other columns stay as they are."""
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    wide = 3 * (cols + gap)
+    buf = torch.full((rows, wide), 9.0, device="cuda").to(_torch_dtype(dtype))
+    x, out, dy = (buf[:, k * (cols + gap):k * (cols + gap) + cols] for k in range(3))
+    x.copy_(torch.randn((rows, cols), device="cuda"))
+    dy.copy_(torch.randn((rows, cols), device="cuda"))
+    w = torch.randn(cols, device="cuda")
+    want, mean, rstd = pg.layer_norm(x.clone(), w, stats=True)
+    want_b = pg.layer_norm_backward(dy.clone(), x.clone(), mean, rstd, w)
+    before = buf.clone()
+    assert pg.layer_norm(x, w, None, out) is out and torch.equal(out, want)
+    got = pg.layer_norm_backward(dy, x, mean, rstd, w, out)
+    assert all(torch.equal(a, b) for a, b in zip(got, want_b))
+    out.copy_(before[:, cols + gap:2 * cols + gap])
+    assert torch.equal(buf, before)
+    with pytest.raises(ValueError, match="overlaps x"):
+        pg.layer_norm(x, w, None, buf[:, 1:cols + 1])
+    assert pg.device_status() == (0, 0)

@@ -475,3 +475,23 @@ def test_eps_beyond_the_norm_of_some_matrices():
         for b in range(5):
             assert _rel(o[b], _exact(g[b], eps=np.float32(1e-7).item())) <= _tol("f32", g[b])
             assert torch.equal(o[b], pg.orthogonalize(g[b])) or m > 128  # larger ones may be cut otherwise
+
+
+@pytest.mark.parametrize("m,n", [(60, 96), (200, 136), (130, 131)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_slice_of_the_same_buffer_may_be_the_output(m, n, dtype):
+    """G and out side by side in one buffer: as columns, and as matrices."""
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    g = torch.stack([_gradient(m, n, "flat", b) for b in range(3)]).to(_torch_dtype(dtype))
+    want = pg.orthogonalize(g)
+    for buf in (torch.full((3, m, 2 * n), 7.0, dtype=g.dtype, device="cuda"),
+                torch.full((3, 2 * m, n), 7.0, dtype=g.dtype, device="cuda")):
+        columns = buf.shape[2] > n
+        G, out = (buf[:, :, :n], buf[:, :, n:]) if columns else (buf[:, :m], buf[:, m:])
+        G.copy_(g)
+        assert pg.orthogonalize(G, out) is out
+        assert torch.equal(out, want) and torch.equal(G, g)
+        with pytest.raises(ValueError, match="overlaps G"):
+            pg.orthogonalize(G, buf[:, :, 1:n + 1] if columns else buf[:, 1:m + 1])
+    _check_status()

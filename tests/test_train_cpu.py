@@ -125,3 +125,38 @@ def test_sides_beyond_a_c_int_are_refused(lib, shape):
     import torch
     with pytest.raises(ValueError, match="2\\^31 - 1"):
         pg.orthogonalize(torch.empty(shape, device="meta"))
+
+
+def _bytes_of(view):
+    address, batch, m, n, ld, pitch, size = view
+    return {address + (b * pitch + i * ld + j) * size + k
+            for b in range(batch) for i in range(m) for j in range(n) for k in range(size)}
+
+
+def test_shared_bytes():
+    """Against the sets of bytes: never missed, and siblings told apart."""
+    import random
+
+    from async_copy_pipelined_gb300 import training
+    rng = random.Random(1)
+    found = {True: 0, False: 0}
+    for _ in range(4000):
+        views = []
+        for k in range(2):
+            batch, m, n = rng.choice((1, 1, 2, 3)), rng.choice((1, 2, 3, 4)), rng.randint(1, 5)
+            ld = n + rng.choice((0, 0, 1, 5, n))
+            pitch = rng.choice((ld * m, ld * m + 3, 2 * ld * m, n, 0)) if batch > 1 else ld * (m - 1) + n
+            views.append((rng.randint(0, 60) * 2, batch, m, n, ld if m > 1 else n, pitch, rng.choice((2, 4))))
+            if k == 1 and rng.random() < 0.6:  # a sibling: the same pitches and type
+                views[1] = (views[1][0], *views[0][1:3], min(views[1][3], views[0][4]), *views[0][4:])
+        shared = bool(_bytes_of(views[0]) & _bytes_of(views[1]))
+        said = training._share_bytes(*views)
+        assert said or not shared, views
+        found[said] += 1
+    assert min(found.values()) > 500
+    for other, shared in (((8, 3, 4, 8, 16, 64, 1), False), ((4, 3, 4, 8, 16, 64, 1), True),
+                          ((64 * 3, 3, 4, 8, 16, 64, 1), False), ((8, 1, 1, 8, 8, 8, 1), False)):
+        assert training._share_bytes((0, 3, 4, 8, 16, 64, 1), other) == shared
+    # neighbours in a buffer of matrices side by side, and one after the other
+    assert not training._share_bytes((0, 3, 4, 8, 8, 64, 2), (64, 3, 4, 8, 8, 64, 2))
+    assert training._share_bytes((0, 3, 4, 8, 8, 64, 2), (62, 3, 4, 8, 8, 64, 2))
