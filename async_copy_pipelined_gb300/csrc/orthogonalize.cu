@@ -1381,7 +1381,9 @@ int orthogonalize(int batch, int m, int n, const void *G, long long ldg, long lo
     if (!empty) {
         if (ldg < n || ldo < n || !G || !out)
             return GEMM_ERR_INVALID_ARG;
-        if (batch > 1 && (g_batch < 0 || o_batch < ldo * (m - 1) + n))
+        // One matrix of out after the other, or row by row in turn.
+        if (batch > 1 && (g_batch < 0 || (o_batch < ldo * (m - 1) + n &&
+                                          (o_batch < n || ldo < o_batch * (batch - 1) + n))))
             return GEMM_ERR_INVALID_ARG;
         const uintptr_t ga = dtype == GEMM_DTYPE_F32 ? 3u : 1u, oa = out_dtype == GEMM_DTYPE_F32 ? 3u : 1u;
         if ((reinterpret_cast<uintptr_t>(G) & ga) != 0 || (reinterpret_cast<uintptr_t>(out) & oa) != 0 ||

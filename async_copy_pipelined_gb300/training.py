@@ -398,7 +398,7 @@ def orthogonalize(G, out=None, *, steps=5, coefficients=COEFFICIENTS, eps=1e-7, 
         if _share_bytes((out.data_ptr(), batch, m, n, ldo, o_batch, out.element_size()),
                         (G.data_ptr(), batch, m, n, ldg, g_batch, G.element_size())):
             raise ValueError("out overlaps G in memory; it may only be G itself")
-    if batch > 1 and out.numel() and o_batch < ldo * (m - 1) + n:
+    if batch > 1 and out.numel() and o_batch < ldo * (m - 1) + n and (o_batch < n or ldo < o_batch * (batch - 1) + n):
         raise ValueError("the matrices of out overlap in memory")
     triples = _triples(tuple(tuple(c) if hasattr(c, "__len__") else c for c in coefficients), steps)
     l = _lib()

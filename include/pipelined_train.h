@@ -115,9 +115,10 @@ int layer_norm_backward_workspace(int rows, int cols, size_t *bytes);
  *                 is done); sides to 2^20, m n below 2^31, batch to 65535.
  *   G             matrix b, element (i, j) at G[b*g_batch + i*ldg + j], of
  *                 `dtype`; ldg >= n, any alignment.
- *   out           likewise with ldo, o_batch, of `out_dtype`; may be G
- *                 itself (pointer, pitches and type), otherwise shares no
- *                 byte with it.  The products run in the precision this type
+ *   out           likewise with ldo, o_batch, of `out_dtype`, its matrices one
+ *                 after the other or row by row in turn; may be G itself
+ *                 (pointer, pitches and type), otherwise shares no byte with
+ *                 it.  The products run in the precision this type
  *                 asks for, on float16 planes with float32 sums: what they
  *                 add to bfloat16's rounding stays below it for
  *                 GEMM_DTYPE_BF16, and is that of float32 arithmetic for

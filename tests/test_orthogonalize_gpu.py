@@ -495,3 +495,24 @@ def test_a_slice_of_the_same_buffer_may_be_the_output(m, n, dtype):
         with pytest.raises(ValueError, match="overlaps G"):
             pg.orthogonalize(G, buf[:, :, 1:n + 1] if columns else buf[:, 1:m + 1])
     _check_status()
+
+
+@pytest.mark.parametrize("batch,m,n", [(3, 60, 96), (2, 200, 136), (4, 1, 40), (5, 33, 700), (3, 300, 131)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_matrices_row_by_row_in_turn(batch, m, n, dtype):
+    """A (m, batch, n) buffer seen as a stack: for G, for out, and in place."""
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    g = torch.stack([_gradient(m, n, "flat", b) for b in range(batch)]).to(_torch_dtype(dtype))
+    want = pg.orthogonalize(g)
+    buf = torch.full((m, batch, n + 8), 7.0, dtype=g.dtype, device="cuda")
+    view = buf[:, :, :n].transpose(0, 1)
+    assert torch.equal(pg.orthogonalize(g, view), want)
+    assert torch.equal(view, want)
+    view.copy_(g)
+    assert torch.equal(pg.orthogonalize(view), want)
+    pg.orthogonalize(view, view)
+    assert torch.equal(view, want)
+    view.fill_(7.0)
+    assert (buf == 7.0).all()
+    _check_status()

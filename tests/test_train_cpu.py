@@ -160,3 +160,14 @@ def test_shared_bytes():
     # neighbours in a buffer of matrices side by side, and one after the other
     assert not training._share_bytes((0, 3, 4, 8, 8, 64, 2), (64, 3, 4, 8, 8, 64, 2))
     assert training._share_bytes((0, 3, 4, 8, 8, 64, 2), (62, 3, 4, 8, 8, 64, 2))
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(ldo=32, ob=16, eps=-1.0), INVALID), (dict(ldo=32, ob=16, out=514), MISALIGNED),
+    (dict(ldo=31, ob=16, out=514), INVALID), (dict(ldo=32, ob=15, out=514), INVALID),
+    (dict(batch=3, ldo=47, ob=16, out=514), INVALID), (dict(batch=3, ldo=48, ob=16, out=514), MISALIGNED),
+])
+def test_orthogonalize_rows_in_turn(lib, kw, status):
+    """out's matrices row by row in turn: its pitches are right (the next
+    check speaks) unless rows overlap."""
+    assert _orthogonalize(lib, **kw) == status
