@@ -411,6 +411,8 @@ def orthogonalize(G, out=None, *, steps=5, coefficients=COEFFICIENTS, eps=1e-7, 
         ws = workspace
         if ws.device != device:
             raise ValueError(f"workspace is on {ws.device}, G on {device}")
+        if not ws.is_contiguous():
+            raise ValueError("workspace must be contiguous")
     _call(device, "orthogonalize", l.orthogonalize, batch, m, n, G.data_ptr(), ldg, g_batch, dt, out.data_ptr(), ldo,
           o_batch, odt, steps, triples, eps, ws.data_ptr(),
           ws.numel() * ws.element_size(), handle)

@@ -516,3 +516,18 @@ def test_matrices_row_by_row_in_turn(batch, m, n, dtype):
     view.fill_(7.0)
     assert (buf == 7.0).all()
     _check_status()
+
+
+def test_a_workspace_with_gaps_or_repeats_is_refused():
+    """numel() of a view that is not contiguous says nothing of the memory
+    behind its address."""
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    g = _gradient(200, 300, "flat", 1)
+    one = torch.empty(256, dtype=torch.uint8, device="cuda")
+    for ws in (one.expand(1 << 16, 256), torch.empty((1 << 20, 32), dtype=torch.uint8, device="cuda")[:, :16]):
+        with pytest.raises(ValueError, match="contiguous"):
+            pg.orthogonalize(g, workspace=ws)
+    assert _rel(pg.orthogonalize(g, workspace=torch.empty((1 << 16, 256), dtype=torch.uint8, device="cuda")),
+                _exact(g)) <= _tol("f32", g)
+    _check_status()
