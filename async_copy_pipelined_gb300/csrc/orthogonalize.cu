@@ -1299,9 +1299,12 @@ int run(const Call &call, const Layout &l, uint8_t *ws, const Device &d, unsigne
     return GEMM_OK;
 }
 
-// Whether the iteration stays where the planes can hold it: from singular
-// values in [0, 1], every step's values within [0, 2] and Q within 15
-// (30 with g below 2).
+// Whether the iteration stays where the planes can hold it: with singular
+// values x in [0, top] before a step, top 1 at first, and q = a + b x x + c x^4,
+// Q is at most 15.5 (31 with g below 2), A + (b / 2c) I at most 7.98, and x q,
+// what the step leaves, at most 2.8, which a next A holds; all under 65504 at
+// their scales, with room for rounding.  The largest values are at the ends
+// and where the derivatives vanish.
 int check_coefficients(const float *coefficients, int steps)
 {
     double top = 1.0;
@@ -1311,16 +1314,29 @@ int check_coefficients(const float *coefficients, int steps)
             return GEMM_ERR_INVALID_ARG;
         if (c != 0.0 && std::fabs(b) > 8.0 * std::fabs(c))
             return GEMM_ERR_UNSUPPORTED; // completing the square would cancel
-        double next = 0.0;
-        constexpr int kSamples = 256;
-        for (int i = 0; i <= kSamples; ++i) {
-            const double x = top * i / kSamples, y = x * x;
-            const double q = a + b * y + c * y * y;
-            if (std::fabs(q) > 15.0)
-                return GEMM_ERR_UNSUPPORTED;
-            next = std::max(next, std::fabs(x * q));
+        const double end = top * top;
+        double most = 0.0, next = 0.0; // of |q| and |x q|
+        auto at = [&](double y) {
+            if (y >= 0.0 && y <= end) {
+                const double q = std::fabs(a + b * y + c * y * y);
+                most = std::max(most, q);
+                next = std::max(next, std::sqrt(y) * q);
+            }
+        };
+        at(0.0);
+        at(end);
+        if (c != 0.0) {
+            at(-b / (2.0 * c)); // q'
+            const double d = 9.0 * b * b - 20.0 * a * c; // (x q)' = a + 3 b y + 5 c y y
+            if (d >= 0.0) {
+                at((-3.0 * b + std::sqrt(d)) / (10.0 * c));
+                at((-3.0 * b - std::sqrt(d)) / (10.0 * c));
+            }
+        } else if (b != 0.0) {
+            at(-a / (3.0 * b));
         }
-        if (next > 1.99)
+        const double shift = c != 0.0 ? b / (2.0 * c) : 0.0;
+        if (most > 15.5 || next > 2.8 || std::max(std::fabs(shift), std::fabs(end + shift)) > 7.98)
             return GEMM_ERR_UNSUPPORTED;
         top = next;
     }

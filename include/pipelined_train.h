@@ -125,9 +125,10 @@ int layer_norm_backward_workspace(int rows, int cols, size_t *bytes);
  *                 GEMM_DTYPE_F32 (at about four times the time).
  *   steps         1 .. 32.
  *   coefficients  3 * steps floats in host memory: a, b, c of each step.
- *                 c = 0 or |b| <= 8 |c|, and from singular values in [0, 1]
- *                 no step may leave [-1.99, 1.99], or reach 15 in
- *                 a + b s + c s s; else GEMM_ERR_UNSUPPORTED.
+ *                 c = 0 or |b| <= 8 |c|, and from singular values x in
+ *                 [0, 1] no step may leave [-2.8, 2.8], or pass 15.5 in
+ *                 a + b x^2 + c x^4 or 7.98 in x^2 + b / 2c; else
+ *                 GEMM_ERR_UNSUPPORTED.
  *   eps           >= 0, finite.  A zero G gives zeros (NaN with eps 0).
  *   workspace     device memory of at least orthogonalize_workspace() bytes,
  *                 256-byte aligned; needs no initialisation, holds nothing

@@ -531,3 +531,29 @@ def test_a_workspace_with_gaps_or_repeats_is_refused():
     assert _rel(pg.orthogonalize(g, workspace=torch.empty((1 << 16, 256), dtype=torch.uint8, device="cuda")),
                 _exact(g)) <= _tol("f32", g)
     _check_status()
+
+
+STEEP = [(8.28721201814563, -23.595886519098837, 17.300387312530933),
+         (4.107059111542203, -2.9478499167379106, 0.5448431082926601),
+         (3.9486908534822946, -2.908902115962949, 0.5518191394370137),
+         (3.3184196573706015, -2.488488024314874, 0.51004894012372),
+         (2.300652019954817, -1.6689039845747493, 0.4188073119525673)]
+
+
+@pytest.mark.parametrize("m,n", [(100, 180), (200, 330), (700, 300)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("coefficients", [STEEP, [(2.7, 0.0, 0.0), (1.0, -0.24, 0.03)]])
+def test_steps_that_pass_two(m, n, dtype, coefficients):
+    """Singular values near 2 and up to 2.7 on the way: a matrix of one strong
+    direction, whose value starts at 1, over weak ones."""
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    coefficients = [tuple(float(np.float32(v)) for v in c) for c in coefficients]
+    g = _gradient(m, n, "flat", 5, scale=0.02)
+    torch.manual_seed(m)
+    u, v = (torch.nn.functional.normalize(torch.randn(k, device="cuda"), dim=0) for k in (m, n))
+    g = (g + 40.0 * u[:, None] * v).to(_torch_dtype(dtype))
+    o = pg.orthogonalize(g, steps=len(coefficients), coefficients=coefficients)
+    assert o.isfinite().all()
+    assert _rel(o, _exact(g, len(coefficients), coefficients)) <= _tol(dtype, g)
+    _check_status()

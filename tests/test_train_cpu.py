@@ -171,3 +171,20 @@ def test_orthogonalize_rows_in_turn(lib, kw, status):
     """out's matrices row by row in turn: its pitches are right (the next
     check speaks) unless rows overlap."""
     assert _orthogonalize(lib, **kw) == status
+
+
+# A schedule of five steps whose first peaks at 1.9917 (Polar Express).
+STEEP = (8.28721201814563, -23.595886519098837, 17.300387312530933, 4.107059111542203, -2.9478499167379106,
+         0.5448431082926601, 3.9486908534822946, -2.908902115962949, 0.5518191394370137, 3.3184196573706015,
+         -2.488488024314874, 0.51004894012372, 2.300652019954817, -1.6689039845747493, 0.4188073119525673)
+
+
+@pytest.mark.parametrize("steps,co,status", [
+    (1, STEEP[:3], MISALIGNED), (5, STEEP, MISALIGNED), (1, (2.79, 0.0, 0.0), MISALIGNED), (1, (2.81, 0.0, 0.0), 3),
+    (1, (5.3, -8.0, 4.0), MISALIGNED), (2, (2.7, 0.0, 0.0, 0.3, 0.08, 0.01), 3),
+    (2, (2.7, 0.0, 0.0, 0.9, -0.08, 0.01), MISALIGNED),  # x x + b / 2c ends at 11.3 and at 3.3
+    (1, (15.6, -42.0, 28.0), 3), (1, (0.0, 0.0, 0.0), MISALIGNED),
+])
+def test_orthogonalize_coefficients(lib, steps, co, status):
+    """Accepted ones come to the next check, of an address."""
+    assert _orthogonalize(lib, steps=steps, co=co, out=514) == status
