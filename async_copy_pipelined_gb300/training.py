@@ -285,12 +285,13 @@ def layer_norm(x, weight=None, bias=None, out=None, *, eps=1e-5, stats=False, st
     return (out, mean, rstd) if stats else out
 
 
-def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, *, stream=None):
+def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, *, bias=None, stream=None):
     """(dx, dweight, dbias) of layer_norm from dy, its input x, the mean and
     rstd it returned, and its weight.
 
-    dx has x's type; dweight and dbias have weight's type and are None when
-    weight is None.  All sums are float32 in an order fixed by the sizes: the
+    dx has x's type; dweight and dbias have weight's.  Without a weight
+    dweight is None, and dbias too unless bias, the one layer_norm was given,
+    says that there is one (its values are not read).  All sums are float32 in an order fixed by the sizes: the
     same inputs give the same bits.  out: where dx goes (dy or x itself for an
     in-place call); allocated if None."""
     torch = _load()
@@ -324,13 +325,20 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, *, stream=None
     l = _lib()
     wdt, ws_bytes = F32, 0
     dweight = dbias = ws = pdw = pdb = pws = None
-    if weight is not None:
-        wdt = _dtype(weight, "weight")
-        dweight = torch.empty_like(weight)
-        dbias = torch.empty_like(weight)
+    parameter = weight if weight is not None else bias
+    if bias is not None:
+        _vector(bias, "bias", rows[1], device)
+        if bias.dtype != parameter.dtype:
+            raise TypeError("weight and bias must have one type")
+    if parameter is not None:
+        wdt = _dtype(parameter, "weight" if weight is not None else "bias")
+        if weight is not None:
+            dweight = torch.empty_like(weight)
+            pdw = dweight.data_ptr()
+        dbias = torch.empty_like(parameter)
         ws = _workspace(device, _norm_bytes(device, rows[0], rows[1]), other)
         ws_bytes = ws.numel()
-        pdw, pdb, pws = dweight.data_ptr(), dbias.data_ptr(), ws.data_ptr()
+        pdb, pws = dbias.data_ptr(), ws.data_ptr()
     _call(device, "layer_norm_backward", l.layer_norm_backward, rows[0], rows[1], dy.data_ptr(), dy_rows[2],
           x.data_ptr(), rows[2], dt, mean.data_ptr(), rstd.data_ptr(), pw, wdt, out.data_ptr(), lddx, pdw, pdb, pws,
           ws_bytes, handle)

@@ -542,3 +542,30 @@ def test_a_slice_of_the_same_buffer_may_be_the_output(rows, cols, gap, dtype):
     with pytest.raises(ValueError, match="overlaps x"):
         pg.layer_norm(x, w, None, buf[:, 1:cols + 1])
     assert pg.device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("rows,cols", [(0, 8), (1, 300), (30, 1000), (400, 1000), (9000, 264), (700, 8200), (3, 20000)])
+@pytest.mark.parametrize("dtype,bdtype", [("f32", "f32"), ("bf16", "f32"), ("f32", "bf16")])
+def test_the_gradient_of_a_bias_alone(rows, cols, dtype, bdtype):
+    """layer_norm takes a bias without a weight, and so does its gradient."""
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    x, x64, _ = _make(rows, cols, dtype, 0, seed=rows + cols)
+    dy, dy64, _ = _make(rows, cols, dtype, 0, seed=rows + cols + 1)
+    b, _ = _vec(cols, bdtype, 8, 0.0)
+    _, mean, rstd = pg.layer_norm(x, None, b, eps=EPS, stats=True)
+    dx, dw, db = pg.layer_norm_backward(dy, x, mean, rstd, bias=b)
+    assert dw is None and db.dtype == b.dtype and db.shape == b.shape
+    m64, r64 = mean.double().cpu().numpy(), rstd.double().cpu().numpy()
+    want, bound = _backward_bounds(dy64, x64, m64, r64, np.ones(cols), dtype, bdtype)
+    _close(dx.double().cpu().numpy(), want[0], bound[0], "dx")
+    _close(db.double().cpu().numpy(), want[2], bound[2], "dbias")
+    assert torch.equal(dx, pg.layer_norm_backward(dy, x, mean, rstd)[0])
+    w, _ = _vec(cols, bdtype, 9, 1.0)
+    both = pg.layer_norm_backward(dy, x, mean, rstd, w, bias=b)
+    assert all(torch.equal(p, q) for p, q in zip(both, pg.layer_norm_backward(dy, x, mean, rstd, w)))
+    with pytest.raises(TypeError):
+        pg.layer_norm_backward(dy, x, mean, rstd, w, bias=b.half())
+    with pytest.raises(ValueError, match="bias must be"):
+        pg.layer_norm_backward(dy, x, mean, rstd, bias=torch.ones(cols + 1, device="cuda"))
+    assert pg.device_status() == (0, 0)
