@@ -557,3 +557,32 @@ def test_steps_that_pass_two(m, n, dtype, coefficients):
     assert o.isfinite().all()
     assert _rel(o, _exact(g, len(coefficients), coefficients)) <= _tol(dtype, g)
     _check_status()
+
+
+@pytest.mark.parametrize("m,n", [(1, 50), (20, 30), (64, 64), (100, 300), (128, 1000), (129, 127), (300, 200),
+                                 (700, 300), (500, 1500), (1000, 3000), (2100, 900)])
+@pytest.mark.parametrize("kind", ["flat", "decay", "spaced"])
+def test_float32_results_err_like_float32_arithmetic(m, n, kind):
+    """Not only within the bound above, which accumulators added by truncation
+    meet too: at most one and a half times as far from float64 as the formula
+    in float32 arithmetic, plus 2^-21 for the 22 bits of two planes."""
+    import torch
+    import async_copy_pipelined_gb300 as pg
+    assert torch.get_float32_matmul_precision() == "highest" and not torch.backends.cuda.matmul.allow_tf32
+    if kind == "spaced":  # singular values from 1 to 1e-3
+        torch.manual_seed(m + n)
+        r = min(m, n)
+        u, v = (torch.linalg.qr(torch.randn((k, r), device="cuda").double())[0] for k in (m, n))
+        g = ((u * torch.logspace(0, -3, r, device="cuda").double()) @ v.T).float()
+    else:
+        g = _gradient(m, n, kind, m + n)
+    want = _exact(g)
+    x = g.T if m > n else g
+    x = x / (x.square().sum().sqrt() + 1e-7)
+    for _ in range(5):
+        a, b, c = TRIPLE
+        s = x @ x.T
+        x = a * x + (b * s + c * (s @ s)) @ x
+    plain = _rel(x.T if m > n else x, want)
+    assert _rel(pg.orthogonalize(g), want) <= 1.5 * plain + 2.0 ** -21
+    _check_status()
