@@ -163,7 +163,24 @@ __global__ void __launch_bounds__(32 * kFinishRows) finish_kernel(const Backward
         store_f32(out, p.weight_bf16, column, t);
 }
 
-constexpr long long kAloneElements = 32768;
+// A gradient of few rows goes to one CTA, which needs no second kernel to add
+// up column sums.  Each turn of the CTA's groups takes it 1.1 us, where all
+// turns at once and the second kernel take the device 4 to 6 us whatever their
+// number; but the second launch takes the host 3 to 4 us.  So one CTA has as
+// many turns as cost the device no more than the launch costs the host.
+// bfloat16, microseconds on the device (a call in a loop), one CTA and two
+// kernels:
+//   turns      2                      4                       8
+//   64 columns 4.2 (20.3)  3.9 (24.5) 8.1 (20.0)  4.1 (23.4) 12.5 (20.0) 4.2 (23.2)
+//   1024       5.7 (19.5)  5.0 (23.2) 8.9 (19.9)  5.1 (23.9) 13.2 (20.1) 5.4 (22.7)
+//   2048       6.5 (20.6)  5.0 (23.2) 9.8 (20.3)  5.0 (23.3) 14.0 (20.6) 5.2 (24.0)
+//   4096       8.3 (19.5)  5.7 (23.4) 12.0 (20.3) 5.9 (23.4) 16.9 (20.0) 6.1 (23.2)
+// Of longer rows only one by itself (a second kernel would add up nothing).
+bool one_cta(int rows, int cols)
+{
+    const int at_once = kBackwardThreads / ((cols + 16 * 32 - 1) / (16 * 32) * 32);
+    return rows <= (cols <= 1024 ? 4 : 2) * at_once;
+}
 
 // Most partial sums of a column that any variant makes.
 int backward_parts(int rows, int sms)
@@ -256,14 +273,8 @@ int launch_backward(Backward p, const Device &d, cudaStream_t s)
                          vector_parameter(p.weight);
     // 16 elements leave room for the two column sums of each in registers.
     const int e = p.cols <= 8192 ? 16 : 32;
-    // A gradient of few elements goes to one CTA, which needs no second kernel
-    // to add up column sums.  32 x 1024 bfloat16 rows take it 8.5 us on the
-    // device and two kernels 5.2, but calls of this size wait for the host,
-    // which needs 20 us for one launch and 24 for two.
-    // Not where its groups would take many rows in turn (500 x 64: 39 us).
-    const int at_once = std::max(1, kBackwardThreads / ((p.cols + 16 * 32 - 1) / (16 * 32) * 32));
-    const bool alone = static_cast<long long>(p.rows) * p.cols <= kAloneElements && p.rows <= 8 * at_once;
-    Plan plan = spread(p.rows, p.cols, e, kBackwardThreads, 2, 1, vectors, e == 16, sizeof(T), d, alone ? 1 : d.sms);
+    Plan plan = spread(p.rows, p.cols, e, kBackwardThreads, 2, 1, vectors, e == 16, sizeof(T), d,
+                       one_cta(p.rows, p.cols) ? 1 : d.sms);
     if (plan.elements != 0 && p.rows > 0) {
         p.parts = plan.grid;
         const int st = launch_backward_rows(p, kBf16, plan, d, s);

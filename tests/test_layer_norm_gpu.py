@@ -569,3 +569,14 @@ def test_the_gradient_of_a_bias_alone(rows, cols, dtype, bdtype):
     with pytest.raises(ValueError, match="bias must be"):
         pg.layer_norm_backward(dy, x, mean, rstd, bias=torch.ones(cols + 1, device="cuda"))
     assert pg.device_status() == (0, 0)
+
+
+# Rows on both sides of where a gradient leaves its one CTA.
+FEW = [(r * g, c) for c, g in ((1, 16), (64, 16), (500, 16), (513, 8), (1024, 8), (1025, 5), (2048, 4), (5000, 1),
+                               (8192, 1), (8193, 1), (16384, 1)) for r in (1, 2, 3, 4, 5)]
+
+
+@pytest.mark.parametrize("rows,cols", FEW)
+@pytest.mark.parametrize("dtype,pad", [("f32", 0), ("bf16", 0), ("bf16", 3)])
+def test_few_rows_backward(rows, cols, dtype, pad):
+    test_backward(rows, cols, dtype, "f32", pad, 0)
