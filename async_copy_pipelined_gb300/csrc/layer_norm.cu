@@ -192,9 +192,10 @@ int backward_parts(int rows, int sms)
 // Elements per thread `e`, rows at a time, and where they come from.  The
 // ring pays once a group has several rows to run ahead over; below that the
 // threads load their own.  `ctas`: how many share the rows.  `full`: there is
-// a variant for rows without a rest.
+// a variant for rows without a rest.  `ragged`: how the ring takes unaligned
+// rows.
 Plan spread(long long rows, int cols, int e, int max_threads, int streams, int parameters, bool vectors, bool full,
-            size_t size, const Device &d, int ctas)
+            Source ragged, size_t size, const Device &d, int ctas)
 {
     Plan plan = {};
     const int tpr = (cols + e * 32 - 1) / (e * 32) * 32;
@@ -211,7 +212,7 @@ Plan spread(long long rows, int cols, int e, int max_threads, int streams, int p
     const int slots = std::min({kMaxSlots, std::max(2, kRingBytes / layer), (kSmemBytes - fixed) / layer});
     const bool ring = trips > 2 * ctas && slots >= 2;
     plan.source = !ring ? (vectors ? kVector : kScalar)
-                  : !vectors ? kRingShifted
+                  : !vectors ? ragged
                   : cols == tpr * e && full ? kRingFull : kRingVector;
     plan.shape = Shape{tpr, groups, slots, slot_bytes, d.status, call_wait_limit_ns(), call_withhold()};
     plan.grid = static_cast<int>(std::min<long long>(trips, ctas));
@@ -236,9 +237,9 @@ int launch_forward(const Forward &p, const Device &d, cudaStream_t s)
     // 16 elements a thread give a single row the most threads; 32 give many
     // rows the most groups, whose reductions overlap.
     const int e = p.cols <= 512 || (p.rows <= 2 * d.sms && p.cols <= 8192) ? 16 : 32;
-    Plan plan = spread(p.rows, p.cols, e, forward_threads(e), 1, 2, vectors, true, sizeof(T), d, d.sms);
+    Plan plan = spread(p.rows, p.cols, e, forward_threads(e), 1, 2, vectors, true, kRingShifted, sizeof(T), d, d.sms);
     if (plan.source == kScalar && e == 32 && p.cols <= 8192)
-        plan = spread(p.rows, p.cols, 16, forward_threads(16), 1, 2, vectors, true, sizeof(T), d, d.sms);
+        plan = spread(p.rows, p.cols, 16, forward_threads(16), 1, 2, vectors, true, kRingShifted, sizeof(T), d, d.sms);
     if (plan.elements != 0) {
         if (!from_ring(plan.source)) // no ring to keep the memory system busy: every CTA that fits
             plan.grid = std::min((p.rows + plan.shape.groups - 1) / plan.shape.groups, 4 * d.sms);
@@ -273,8 +274,8 @@ int launch_backward(Backward p, const Device &d, cudaStream_t s)
                          vector_parameter(p.weight);
     // 16 elements leave room for the two column sums of each in registers.
     const int e = p.cols <= 8192 ? 16 : 32;
-    Plan plan = spread(p.rows, p.cols, e, kBackwardThreads, 2, 1, vectors, e == 16, sizeof(T), d,
-                       one_cta(p.rows, p.cols) ? 1 : d.sms);
+    Plan plan = spread(p.rows, p.cols, e, kBackwardThreads, 2, 1, vectors, e == 16, backward_unaligned(sizeof(T)), sizeof(T),
+                       d, one_cta(p.rows, p.cols) ? 1 : d.sms);
     if (plan.elements != 0 && p.rows > 0) {
         p.parts = plan.grid;
         const int st = launch_backward_rows(p, kBf16, plan, d, s);

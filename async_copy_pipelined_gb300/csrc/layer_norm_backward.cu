@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) backward_rows_kernel(cons
     const long long step = static_cast<long long>(gridDim.x) * shape.groups;
     const long long first = static_cast<long long>(blockIdx.x) * shape.groups + g.index;
     Edges<T, 2> edges;
-    if constexpr (S == kRingShifted) {
+    if constexpr (unaligned(S)) {
         edges.load(ring, g, first);
         edges.place(ring, own, 0);
         edges.load(ring, g, first + step);
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) backward_rows_kernel(cons
     }
     // The bound is the same in the whole group.
     for (long long row = first; row < p.rows; row += step) {
-        if constexpr (S == kRingShifted) {
+        if constexpr (unaligned(S)) {
             edges.place(ring, own, ring.slot + 1 == ring.slots ? 0 : ring.slot + 1);
             edges.load(ring, g, row + 2 * step);
         }
@@ -294,9 +294,11 @@ static int launch_source(const Backward &p, const Plan &plan, const Device &d, c
     if constexpr (E == 16)
         if (plan.source == kRingFull)
             return launch<T, E, kRingFull>(p, plan, d, s);
+    // What spread() was given for unaligned rows.
+    constexpr Source kUnaligned = backward_unaligned(sizeof(T));
     switch (plan.source) {
     case kRingVector: return launch<T, E, kRingVector>(p, plan, d, s);
-    case kRingShifted: return launch<T, E, kRingShifted>(p, plan, d, s);
+    case kUnaligned: return launch<T, E, kUnaligned>(p, plan, d, s);
     case kVector: return launch<T, E, kVector>(p, plan, d, s);
     default: return launch<T, E, kScalar>(p, plan, d, s);
     }

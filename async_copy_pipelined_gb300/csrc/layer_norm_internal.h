@@ -53,6 +53,9 @@ struct Plan {
 constexpr int forward_threads(int elements) { return elements > 16 ? 512 : 768; }
 constexpr int kBackwardThreads = 512;
 
+// How the gradient takes unaligned rows.
+constexpr Source backward_unaligned(size_t size) { return size == 4 ? kRingElement : kRingShifted; }
+
 struct Device {
     int index, sms;
     unsigned long long ctx;

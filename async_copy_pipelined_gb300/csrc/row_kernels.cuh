@@ -4,8 +4,9 @@
 // A group of `tpr` threads (whole warps) takes a row, each thread E of its
 // elements in registers; a CTA holds `groups` groups.  Elements move in 16-byte
 // vectors: straight where the rows are 16-byte aligned; where they are not,
-// through shared memory and shifted (kRingShifted), or, when there are too few
-// rows for a ring, one by one.
+// through shared memory, there shifted (kRingShifted) or read one by one
+// (kRingElement), or, when there are too few rows for a ring, one by one from
+// where they are.
 //
 // Ring: the first thread of each group copies the group's rows into shared
 // memory (bulk copies completing on mbarriers), several ahead of the one being
@@ -45,10 +46,16 @@ constexpr int kRingBytes = 128 * 1024;
 // two 16-byte granules of shared memory it lies in, and a warp's pieces are
 // shifted against each other to the granules of the output: 8192 rows of 8192
 // bfloat16 at a pitch of 8195 take 69 us forward and 122 backward, 142 and 193
-// element by element; in float32 89 and 176, 128 and 164 element by element.
-enum Source { kRingFull, kRingVector, kRingShifted, kVector, kScalar };
-constexpr bool from_ring(Source s) { return s == kRingFull || s == kRingVector || s == kRingShifted; }
-constexpr bool in_vectors(Source s) { return s != kScalar; }
+// element by element; in float32 the forward 89 and 128.
+// kRingElement: the same rows element by element, which for the gradient of
+// float32 rows, two rows read and one written, costs less than their
+// selections: 8192 x 8192 at a pitch of 8195 takes 132 us, shifted 159 (134
+// and 184 where the output has that pitch too); 16384 x 1000 at 1001 40 and
+// 43, 40000 x 33 34 and 50.
+enum Source { kRingFull, kRingVector, kRingShifted, kRingElement, kVector, kScalar };
+constexpr bool unaligned(Source s) { return s == kRingShifted || s == kRingElement; }
+constexpr bool from_ring(Source s) { return s == kRingFull || s == kRingVector || unaligned(s); }
+constexpr bool in_vectors(Source s) { return s != kScalar && s != kRingElement; }
 
 // Floats that a parameter's copy in shared memory takes: whole pieces.
 __host__ __device__ constexpr int parameter_floats(int cols) { return (cols + 7) / 8 * 8; }
@@ -142,7 +149,7 @@ struct Spread {
             }
         } else if (has(k)) {
             const int j = column(k);
-            if constexpr (S == kScalar)
+            if constexpr (!in_vectors(S))
                 v[0] = to_f32(row.at[j]);
             else
                 Vec16<T>::unpack(*reinterpret_cast<const uint4 *>(row.at + j), v);
@@ -220,8 +227,10 @@ struct Spread {
         if constexpr (kPiece == 8) {
             Vec16<float>::unpack(*reinterpret_cast<const uint4 *>(copy + j / 2), v);
             Vec16<float>::unpack(*reinterpret_cast<const uint4 *>(copy + half + j / 2), v + 4);
-        } else {
+        } else if constexpr (kPiece == 4) {
             Vec16<float>::unpack(*reinterpret_cast<const uint4 *>(copy + j), v);
+        } else {
+            v[0] = copy[j];
         }
     }
     // A parameter vector as float32 in shared memory, by the whole CTA.  For
@@ -232,8 +241,8 @@ struct Spread {
     __device__ __forceinline__ void copy_parameter(float *copy, const void *p, bool bf16, float absent) const
     {
         // Several loads of a thread in flight: the first rows wait for them.
-        constexpr int kUnit = S == kRingShifted ? 1 : 4, kBatch = 8;
-        const int half = parameter_floats(cols) / 2, there = S == kRingShifted ? 2 * half : cols;
+        constexpr int kUnit = unaligned(S) ? 1 : 4, kBatch = 8;
+        const int half = parameter_floats(cols) / 2, there = unaligned(S) ? 2 * half : cols;
         for (int u0 = threadIdx.x; u0 < there / kUnit; u0 += kBatch * blockDim.x) {
             float v[kBatch][kUnit];
 #pragma unroll

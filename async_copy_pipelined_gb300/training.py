@@ -19,6 +19,7 @@ import async_copy_pipelined_gb300 as _pg
 __all__ = ["layer_norm", "layer_norm_backward", "orthogonalize"]
 
 F32, BF16 = 0, 1  # enum gemm_dtype
+INT_MAX = 0x7FFFFFFF
 
 def bind(l):
     I, L, P, F, S = ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p, ctypes.c_float, ctypes.c_size_t
@@ -73,7 +74,7 @@ def _counts(name, *sizes):
     """Sizes that the library takes as C ints, of which ctypes would silently
     keep the lower 32 bits."""
     for n in sizes:
-        if n > 0x7FFFFFFF:
+        if n > INT_MAX:
             raise ValueError(f"{name} has a size of {n}: at most 2^31 - 1")
 
 
@@ -87,7 +88,8 @@ def _rows(t, name):
     if cols < 1:
         raise ValueError(f"{name} has empty rows")
     count = t.numel() // cols
-    _counts(name, count, cols)
+    if count > INT_MAX or cols > INT_MAX:
+        _counts(name, count, cols)
     if t.is_contiguous():
         return count, cols, cols
     stride = t.stride()
