@@ -274,8 +274,9 @@ int launch_backward(Backward p, const Device &d, cudaStream_t s)
                          vector_parameter(p.weight);
     // 16 elements leave room for the two column sums of each in registers.
     const int e = p.cols <= 8192 ? 16 : 32;
-    Plan plan = spread(p.rows, p.cols, e, kBackwardThreads, 2, 1, vectors, e == 16, backward_unaligned(sizeof(T)), sizeof(T),
-                       d, one_cta(p.rows, p.cols) ? 1 : d.sms);
+    const int ctas = one_cta(p.rows, p.cols) ? 1 : d.sms;
+    Plan plan = spread(p.rows, p.cols, e, kBackwardThreads, 2, 1, vectors, e == 16, backward_unaligned(sizeof(T)),
+                       sizeof(T), d, ctas);
     if (plan.elements != 0 && p.rows > 0) {
         p.parts = plan.grid;
         const int st = launch_backward_rows(p, kBf16, plan, d, s);

@@ -31,11 +31,12 @@
 // Measured in float64 arithmetic on spectra from flat to 1e-3 of the largest
 // value (256 .. 1000 rows): the bfloat16 result is off by 1.03 to 1.15 times
 // the error of rounding the exact result; one pair throughout by up to 16
-// times.  float32 result, 1000 x 3000 on GB300: 1.7e-7 for equal singular
+// times.  On GB300 at 8192 x 8192: 1.03 (decaying spectrum) and 1.05 times
+// (flat).  float32 result, 1000 x 3000: 1.7e-7 for equal singular
 // values and 3.3e-6 for log-spaced ones down to 1e-3, where the formula in
 // float32 arithmetic is off by 7.3e-7 and 4.5e-6.  A fifth pair for Q X, x1 of
 // both, takes 5 % more time; without it the error stays below 1.4 times that of
-// float32 arithmetic at every size and spectrum tried.
+// float32 arithmetic at every size and spectrum tried (tests hold it to 1.5).
 //
 // A A is never added to b A: the square is completed,
 //   Q = c (A + (b / 2c) I)^2 + (a - b b / 4c) I,
@@ -84,16 +85,6 @@ struct Pass {
 };
 constexpr int kMaxPasses = 5;
 
-// The tensor cores add to a float32 accumulator by truncation: n additions in
-// a row lose about n 2^-25 of a sum of equal signs (A's diagonal), which a
-// bfloat16 result does not notice and a float32 one does.  There (Product.fine)
-// each K block (four additions) of the one pass over the leading planes has an
-// accumulator of its own, and the epilogue adds them with rounding; the other
-// passes' terms are 2^-11 as large and share one.  Error of the float32 result
-// against float64, 1000 x 3000, flat and decaying spectrum: 9.5e-6 and 1.2e-5
-// with four K blocks to an accumulator, 3.1e-6 and 4.2e-6 with one; the same
-// products in float32 arithmetic give 3.7e-6 and 7.0e-6 (Q X with five pairs).
-
 enum Output { kPlanes, kBf16, kF32 };
 
 struct Maps {
@@ -104,13 +95,25 @@ struct Maps {
     CUtensorMap store, mirror, store_diag, mirror_diag;
 };
 
-// D (rows x cols, a batch of them) = sum over the passes of left plane times
-// right plane over k, scaled by alpha, plus diag on the diagonal.
+// The tensor cores add to a float32 accumulator by truncation: n additions in
+// a row lose about n 2^-25 of a sum of equal signs (A's diagonal), which a
+// bfloat16 result does not notice and a float32 one does.  There (Product.fine)
+// each K block (four additions) of the one pass over the leading planes has an
+// accumulator of its own, and the epilogue adds them with rounding; the other
+// passes' terms are 2^-11 as large and share one.  Error of the float32 result
+// against float64, 1000 x 3000, flat and decaying spectrum, the products then
+// with a fifth pair in Q X: 9.5e-6 and 1.2e-5 with four K blocks to an
+// accumulator, 3.1e-6 and 4.2e-6 with one.  With four pairs and one K block to
+// an accumulator: 3.1e-6 and 4.3e-6, the formula in float32 arithmetic 3.7e-6
+// and 7.0e-6.
+enum Fine { kWhole, kPerBlock, kPerStep }; // one for all, one per K block, one per MMA
+
 // Short sums show what the four additions of a K block lose: with a side r of
 // up to this every MMA has an accumulator of its own.
 constexpr int kStepSide = 128;
 
-enum Fine { kWhole, kPerBlock, kPerStep }; // one for all, one per K block, one per MMA
+// D (rows x cols, a batch of them) = sum over the passes of left plane times
+// right plane over k, scaled by alpha, plus diag on the diagonal.
 
 struct Product {
     int rows, cols, k, batch;
@@ -472,7 +475,8 @@ __global__ void __launch_bounds__(Tile<MH, BN, S, Split>::kThreads, 1)
             auto begin = [&]() { // an accumulator
                 const int slot = acc % T::kAccBufs;
                 const uint32_t use_parity = static_cast<uint32_t>((acc / T::kAccBufs) & 1);
-                if (!__all_sync(0xffffffffu, mbar_wait_bounded(tmem_empty0 + 8u * slot, use_parity ^ 1u, p.wait_limit_ns))) {
+                if (!__all_sync(0xffffffffu,
+                                mbar_wait_bounded(tmem_empty0 + 8u * slot, use_parity ^ 1u, p.wait_limit_ns))) {
                     if (on)
                         record_error(p.status, kErrFamilyOrthogonalize | kErrRoleMma);
                     return false;
@@ -624,7 +628,8 @@ __global__ void __launch_bounds__(Tile<MH, BN, S, Split>::kThreads, 1)
                 if (p.diag != 0.0f && row0 < col0 + 64 && col0 < row0 + 32) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        v[j] = add2(v[j], pair(col0 + 2 * j == row ? diag : 0.0f, col0 + 2 * j + 1 == row ? diag : 0.0f));
+                        v[j] = add2(v[j], pair(col0 + 2 * j == row ? diag : 0.0f,
+                                               col0 + 2 * j + 1 == row ? diag : 0.0f));
                 }
                 uint32_t w[32];
                 float lo, hi;

@@ -57,18 +57,13 @@ __device__ __forceinline__ void load8(const Matrix &p, long long row_at, int j, 
 {
     if (p.vec && j + 8 <= p.n) {
         if (p.bf16) {
-            const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.G) + row_at + j);
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[2 * e] = __uint_as_float(w[e] << 16);
-                v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-            }
+            Vec16<__nv_bfloat16>::unpack(
+                *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.G) + row_at + j), v);
         } else {
-            const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p.G) + row_at + j);
-            const float4 a = q[0], b = q[1];
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const float *>(p.G) + row_at + j);
+            const uint4 a = q[0], b = q[1];
+            Vec16<float>::unpack(a, v);
+            Vec16<float>::unpack(b, v + 4);
         }
     } else {
 #pragma unroll
@@ -230,7 +225,6 @@ struct Call {
         return Matrix{G, dtype == GEMM_DTYPE_BF16, m, n, ldg, g_batch, vec};
     }
 };
-
 
 // bfloat16 results of matrices whose shorter side is at most 128 and whose
 // longer one a cluster of eight CTAs holds (orthogonalize_small.cu).

@@ -207,10 +207,8 @@ struct Spread {
                 Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(q), v);
             } else {
                 const uint2 h = *reinterpret_cast<const uint2 *>(q);
-                v[0] = __uint_as_float(h.x << 16);
-                v[1] = __uint_as_float(h.x & 0xFFFF0000u);
-                v[2] = __uint_as_float(h.y << 16);
-                v[3] = __uint_as_float(h.y & 0xFFFF0000u);
+                unpack_bf16(h.x, v);
+                unpack_bf16(h.y, v + 2);
             }
         } else {
             const float *q = static_cast<const float *>(p) + column(k);
@@ -256,10 +254,8 @@ struct Spread {
                         v[k][0] = load_f32(p, bf16, j);
                     } else if (bf16) {
                         const uint2 h = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + j);
-                        v[k][0] = __uint_as_float(h.x << 16);
-                        v[k][1] = __uint_as_float(h.x & 0xFFFF0000u);
-                        v[k][2] = __uint_as_float(h.y << 16);
-                        v[k][3] = __uint_as_float(h.y & 0xFFFF0000u);
+                        unpack_bf16(h.x, v[k]);
+                        unpack_bf16(h.y, v[k] + 2);
                     } else {
                         Vec16<float>::unpack(*reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + j), v[k]);
                     }
@@ -461,8 +457,8 @@ struct Ring {
     int position = 0; // the next to fill
     bool failed = false;
 
-    __device__ __forceinline__ Ring(uint32_t bars_at, uint32_t slots_base, const Shape &s, const Group &g, int row_bytes_,
-                                    int rows_)
+    __device__ __forceinline__ Ring(uint32_t bars_at, uint32_t slots_base, const Shape &s, const Group &g,
+                                    int row_bytes_, int rows_)
         : bars(bars_at + 8u * kMaxSlots * g.index),
           slots_at(slots_base + static_cast<uint32_t>(g.index * s.slots * Streams * s.slot_bytes)),
           row_bytes(row_bytes_), slot_bytes(s.slot_bytes), slots(s.slots), rows(rows_),

@@ -51,6 +51,13 @@ struct Vec16<float> {
     }
 };
 
+// Two bfloat16 values in a word.
+__device__ __forceinline__ void unpack_bf16(uint32_t w, float *v)
+{
+    v[0] = __uint_as_float(w << 16);
+    v[1] = __uint_as_float(w & 0xFFFF0000u);
+}
+
 template <>
 struct Vec16<__nv_bfloat16> {
     static constexpr int kElements = 8;
@@ -58,10 +65,8 @@ struct Vec16<__nv_bfloat16> {
     {
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[2 * e] = __uint_as_float(w[e] << 16);
-            v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-        }
+        for (int e = 0; e < 4; ++e)
+            unpack_bf16(w[e], v + 2 * e);
     }
     static __device__ __forceinline__ uint4 pack(const float *v)
     {
