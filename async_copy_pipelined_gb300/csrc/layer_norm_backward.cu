@@ -4,11 +4,14 @@
 // is one partial sum per column and CTA, added up by a second small kernel.
 //
 // Measured on GB300 (bytes of dy, x and dx): 16384 x 4096 bfloat16 84 us, 4.8
-// TB/s; 3000 x 5000 float32 41 us, 4.4 TB/s; 16384 x 4096 float32 138 us, 5.8
-// TB/s.  In bfloat16 the instructions bound it (two of four issue slots a clock
-// with a quarter of the warps, whose registers the column sums fill); DRAM is
-// busy 55 % of the time.  Above 8192 columns a CTA holds one row of 32 elements
-// a thread and reads it twice from shared memory: 4096 x 16384 bfloat16 122 us.
+// TB/s; 3000 x 5000 float32 41 us, 4.4 TB/s; 16384 x 4096 float32 137 us, 5.9
+// TB/s.  In bfloat16 nothing is full: DRAM is busy 55 % of the time, two of four
+// issue slots a clock are used.  The sixteen warps that the column sums'
+// registers leave wait, a group at a time, for their loads from the ring and
+// for a row's sums.  Above 8192 columns a CTA holds one row of 32 elements a
+// thread and reads it twice from shared memory: 4096 x 16384 bfloat16 127 us.
+// From 11469 float32 columns on no two rows of x and dy fit the ring, and
+// nothing runs ahead: 5461 x 11468 156 us, x 12288 300.
 #include "layer_norm_internal.h"
 
 namespace pg {

@@ -4,12 +4,17 @@
 // float32 from row to row; otherwise they are loaded beside x.
 //
 // Measured on GB300 (bytes of x and y; a device copy of as many bytes runs at
-// 6.1 TB/s): 16384 x 4096 bfloat16 50 us, 5.4 TB/s; 8192 x 8192 bfloat16 57
-// us, 4.7 TB/s; 16384 x 4096 float32 94 us, 5.7 TB/s.  Neither DRAM (56 % of
-// its cycles at 16384 x 4096 bfloat16) nor the schedulers (1.5 of 4
-// instructions a clock) are full: what is left is a row's two reductions in a
-// row, which the few rows at a time that registers allow hide in part.  One
-// row is the launch: 4096 bfloat16 take about 3 us on the device.
+// 6.1 TB/s): 16384 x 4096 bfloat16 47 to 50 us, 5.7 to 5.4 TB/s; 8192 x 8192
+// bfloat16 58 us, 4.6 TB/s; 16384 x 4096 float32 94 us, 5.7 TB/s.  Neither DRAM
+// (56 % of its cycles at 16384 x 4096 bfloat16) nor the schedulers (1.5 of 4
+// instructions a clock) are full: a group waits for its row's two sums, one
+// after the other, and the few rows at a time that registers allow hide that in
+// part.  (One sum would do, of each thread's mean and squared differences put
+// together; not tried.)  Longer rows: 4096 x 16384 bfloat16 60 us; float32 has
+// room for two rows in the ring up to 14336 columns, 4096 of them 86 us, of
+// 16384, without, 115; beyond that three passes, 2048 x 32768 bfloat16 131 and
+// float32 219.  One row is the launch: 4096 bfloat16 take about 3 us on the
+// device.
 #include "layer_norm_internal.h"
 
 namespace pg {

@@ -16,10 +16,10 @@
 // row or two to a group there is nothing to run ahead of, and threads load
 // their elements themselves.
 //
-// Beside DRAM it is the instructions issued per element that bound these
-// kernels, so additions and multiplications run on pairs (one instruction for
-// two float32 values), and a thread has enough elements to spread the cost of
-// a row's reductions over.
+// Beside DRAM these kernels spend their time on instructions per element and on
+// waiting for a row's reductions, so additions and multiplications run on pairs
+// (one instruction for two float32 values), and a thread has enough elements to
+// spread the cost of the reductions over.
 #pragma once
 
 #include "gemm_internal.h"
@@ -45,7 +45,7 @@ constexpr int kRingBytes = 128 * 1024;
 // kRingShifted: rows of any alignment and length.  A piece is cut out of the
 // two 16-byte granules of shared memory it lies in, and a warp's pieces are
 // shifted against each other to the granules of the output: 8192 rows of 8192
-// bfloat16 at a pitch of 8195 take 69 us forward and 122 backward, 142 and 193
+// bfloat16 at a pitch of 8195 take 68 us forward and 115 backward, 142 and 193
 // element by element; in float32 the forward 89 and 128.
 // kRingElement: the same rows element by element, which for the gradient of
 // float32 rows, two rows read and one written, costs less than their
