@@ -51,7 +51,9 @@ enum gemm_dtype {
  *   mean, rstd   rows floats each, or both NULL when no gradient is wanted.
  *   eps          >= 0 and finite.
  *
- * A row that holds a NaN or an infinity gives NaN in that row alone.
+ * A row that holds a NaN or an infinity gives NaN in that row alone.  Squared
+ * differences are float32: where they overflow (differences of about 1e19 and
+ * more) rstd is 0 and y the bias.
  */
 int layer_norm(int rows, int cols,
                const void *x, long long ldx, int dtype,
