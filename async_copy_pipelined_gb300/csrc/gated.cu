@@ -101,7 +101,9 @@ __device__ __forceinline__ void activate_with_slope(float g, float &value, float
     } else {
         const float s = sigmoid(2.0f * kTanhScale * g * fmaf(kTanhCubic * g, g, 1.0f));
         value = g * s;
-        slope = fmaf(value * (1.0f - s), 2.0f * kTanhScale * fmaf(3.0f * kTanhCubic * g, g, 1.0f), s);
+        // Beyond 32 the first factor is zero; the other one's g^2 is kept finite for it.
+        const float c = fminf(fabsf(g), 32.0f);
+        slope = fmaf(value * (1.0f - s), 2.0f * kTanhScale * fmaf(3.0f * kTanhCubic * c, c, 1.0f), s);
     }
 }
 
