@@ -74,6 +74,7 @@ static std::atomic<int> g_num_sms[kMaxDevices];
 static std::atomic<unsigned long long> g_hook_wait_limit_ns{0}; // 0: kDefaultWaitLimitNs
 static std::atomic<int> g_hook_withhold{-1};
 static std::atomic<int> g_hook_withhold_handover{0};
+static std::atomic<int> g_hook_withhold_scales{-1};
 static std::atomic<int> g_hook_f32_wide{-1}; // f32_wide_rows mode: -1 model, 0 off, 1 forced
 
 // Unique id of the calling thread's current CUDA context (cuCtxGetId), or 0
@@ -254,6 +255,7 @@ int encode_tensor_map(void *map_out, TensorElement element, const void *base, in
 unsigned long long call_wait_limit_ns() { return hook_wait_limit_ns(); }
 
 int call_withhold() { return g_hook_withhold.load(); }
+int call_withhold_scales() { return g_hook_withhold_scales.load(); }
 
 // ------------------------------------------------------------ sizes
 int f32_threads(int tile, int fill)
@@ -803,6 +805,14 @@ int gemm_selftest_bounded_wait(int timeout_us, void *stream)
 int gemm_testing_withhold_handover(int on)
 {
     g_hook_withhold_handover.store(on ? 1 : 0);
+    return GEMM_OK;
+}
+
+int gemm_testing_withhold_scales(int position)
+{
+    if (position < -1)
+        return GEMM_ERR_INVALID_ARG;
+    g_hook_withhold_scales.store(position);
     return GEMM_OK;
 }
 

@@ -43,6 +43,7 @@ struct Call {
     void *c;
     long long ldc;
     int access;
+    int withhold_scales; // test hook: K block of a CTA whose scales are never announced (-1: none)
 };
 
 // The scales of K blocks, which warp 3 copies ahead of the epilogue into a ring:
@@ -115,8 +116,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sum[j] = 0;
 #pragma unroll 1
             for (int kb = 0; kb < blocks; ++kb, ++acc) {
-                if (!mbar_wait_bounded(scales.full(acc), ScaleRing::parity(acc), p.launch.wait_limit_ns) ||
-                    !acquire(p.launch, b, acc)) {
+                if (!acquire(p.launch, b, acc,
+                             mbar_wait_bounded(scales.full(acc), ScaleRing::parity(acc), p.launch.wait_limit_ns))) {
                     ok = false;
                     break;
                 }
@@ -269,6 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int kb = 0; kb < blocks; ++kb, ++f) {
                 if (!mbar_wait_bounded(scales.empty(f), ScaleRing::parity(f) ^ 1u, p.launch.wait_limit_ns)) {
+                    // Each lane for itself: nothing here needs all of them.
+                    record_error(p.launch.status, p.launch.family | kErrRoleProducer);
                     ok = false;
                     break;
                 }
@@ -289,7 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         cp_async_ca4(to + 512 + lane * 512, from_b[0], 4);
                     from_b[0] += p.b_scale_k;
                 }
-                cp_async_mbar_arrive_noinc(scales.full(f));
+                if (static_cast<int>(f) != p.withhold_scales)
+                    cp_async_mbar_arrive_noinc(scales.full(f));
             }
         }
         cp_async_wait_all();
@@ -633,6 +637,7 @@ extern "C" int gemm_fp8(int M, int N, int K, const void *A, long long lda, int a
     p.c = C;
     p.ldc = ldc;
     p.access = row_access(C, ldc, M, size);
+    p.withhold_scales = call_withhold_scales();
     auto go = [&](auto type, auto vector) {
         using T = decltype(type);
         constexpr bool kVector = decltype(vector)::value;

@@ -148,6 +148,7 @@ int encode_tensor_map(void *map_out, TensorElement element, const void *base, in
 // This call's wait limit and withheld ring position (test hooks included).
 unsigned long long call_wait_limit_ns();
 int call_withhold();
+int call_withhold_scales();
 
 // Status codes recorded on device: low byte = kernel family, next byte = role.
 constexpr unsigned int kErrFamilyF32Tma = 1;

@@ -72,6 +72,15 @@ int gemm_testing_f32_wide_rows(int M, int N, int K, int sms, int mode);
 int gemm_testing_withhold_handover(int on);
 
 /*
+ * gemm_testing_withhold_scales: in every later gemm_fp8 call on pairs of CTAs,
+ * the K block (0, 1, 2, ... counted per CTA over all of its tiles) whose scales
+ * are never announced as copied, so that the warps waiting for them give up
+ * after the wait limit and record GEMM_ERR_TIMEOUT.  -1 restores normal
+ * operation.  Returns GEMM_OK or GEMM_ERR_INVALID_ARG.
+ */
+int gemm_testing_withhold_scales(int position);
+
+/*
  * gemm_testing_f32_piece: the work schedule of the persistent FP32 TMA
  * kernel, computed on the host exactly as the kernel computes it: piece
  * `idx` of CTA `cta` when `ctas` CTAs share `tiles` tiles of `k_slices` K
