@@ -99,6 +99,8 @@ def _bind(l):
     l.gemm_testing_withhold_handover.restype = I
     l.gemm_testing_withhold_scales.argtypes = [I]
     l.gemm_testing_withhold_scales.restype = I
+    l.gemm_testing_refuse_smem_limit.argtypes = [I]
+    l.gemm_testing_refuse_smem_limit.restype = I
     l.gemm_testing_f32_wide.argtypes = [I]
     l.gemm_testing_f32_wide.restype = I
     l.gemm_testing_f32_wide_rows.argtypes = [I, I, I, I, I]

@@ -75,6 +75,7 @@ static std::atomic<unsigned long long> g_hook_wait_limit_ns{0}; // 0: kDefaultWa
 static std::atomic<int> g_hook_withhold{-1};
 static std::atomic<int> g_hook_withhold_handover{0};
 static std::atomic<int> g_hook_withhold_scales{-1};
+static std::atomic<int> g_hook_refuse_smem_limit{0};
 static std::atomic<int> g_hook_f32_wide{-1}; // f32_wide_rows mode: -1 model, 0 off, 1 forced
 
 // Unique id of the calling thread's current CUDA context (cuCtxGetId), or 0
@@ -256,6 +257,7 @@ unsigned long long call_wait_limit_ns() { return hook_wait_limit_ns(); }
 
 int call_withhold() { return g_hook_withhold.load(); }
 int call_withhold_scales() { return g_hook_withhold_scales.load(); }
+bool smem_limit_refused() { return g_hook_refuse_smem_limit.load(std::memory_order_relaxed) != 0; }
 
 // ------------------------------------------------------------ sizes
 int f32_threads(int tile, int fill)
@@ -813,6 +815,12 @@ int gemm_testing_withhold_scales(int position)
     if (position < -1)
         return GEMM_ERR_INVALID_ARG;
     g_hook_withhold_scales.store(position);
+    return GEMM_OK;
+}
+
+int gemm_testing_refuse_smem_limit(int on)
+{
+    g_hook_refuse_smem_limit.store(on ? 1 : 0);
     return GEMM_OK;
 }
 

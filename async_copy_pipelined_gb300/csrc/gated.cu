@@ -913,14 +913,15 @@ int gated_projection_backward(int rows, int width, int hidden, const void *dh, l
     p.launch.maps = n;
     p.launch.first_units = product[0].units();
     p.launch.units = p.launch.first_units + (products > 1 ? product[1].units() : 0);
+    // Ahead of the first launch: a call that fails has enqueued nothing.
+    static std::atomic<unsigned long long> limit_set[kMaxDevices];
+    if (ensure_smem_limit(gated_backward_kernel, kSmem, d.index, d.ctx, limit_set) != GEMM_OK)
+        return GEMM_ERR_CUDA;
     st = activation == GEMM_ACT_SILU   ? launch_slopes<GEMM_ACT_SILU>(sl, d, s)
          : activation == GEMM_ACT_GELU ? launch_slopes<GEMM_ACT_GELU>(sl, d, s)
                                        : launch_slopes<GEMM_ACT_GELU_TANH>(sl, d, s);
     if (st != GEMM_OK)
         return st;
-    static std::atomic<unsigned long long> limit_set[kMaxDevices];
-    if (ensure_smem_limit(gated_backward_kernel, kSmem, d.index, d.ctx, limit_set) != GEMM_OK)
-        return GEMM_ERR_CUDA;
     // Started while the slopes end, for which all but the setting up waits: 45 us
     // to 43 for 1000 x 1000 -> 2700.  Not behind many slopes: 1380 us to 1345 for
     // 8192 x 4096 -> 8192.

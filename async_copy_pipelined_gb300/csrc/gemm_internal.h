@@ -76,10 +76,13 @@ constexpr int kMaxDevices = 64;
 // Raise a kernel's dynamic shared-memory limit once per context rather than
 // on every launch: `done[dev]` holds the id of the context in which it was
 // last raised, so a context created after cudaDeviceReset raises it again.
+bool smem_limit_refused(); // test hook: as if the runtime refused it
 template <class Kernel>
 int ensure_smem_limit(Kernel kernel, int smem, int dev, unsigned long long ctx,
                       std::atomic<unsigned long long> (&done)[kMaxDevices])
 {
+    if (smem_limit_refused())
+        return GEMM_ERR_CUDA;
     if (ctx != 0 && dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_acquire) == ctx)
         return GEMM_OK;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)

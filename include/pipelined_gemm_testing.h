@@ -81,6 +81,14 @@ int gemm_testing_withhold_handover(int on);
 int gemm_testing_withhold_scales(int position);
 
 /*
+ * gemm_testing_refuse_smem_limit: with `on` non-zero, every later call whose
+ * kernel needs its shared-memory limit raised fails there with GEMM_ERR_CUDA,
+ * as if the CUDA runtime had refused it (on the host: no kernel fails).  0
+ * restores normal operation.  Returns GEMM_OK.
+ */
+int gemm_testing_refuse_smem_limit(int on);
+
+/*
  * gemm_testing_f32_piece: the work schedule of the persistent FP32 TMA
  * kernel, computed on the host exactly as the kernel computes it: piece
  * `idx` of CTA `cta` when `ctas` CTAs share `tiles` tiles of `k_slices` K
