@@ -4,7 +4,10 @@
 
 Produces ``async_copy_pipelined_gb300/_build/libpipelined_gemm.so`` and, by g++
 against the installed torch, the feed-forward operators' native binding
-``_build/_feedforward.so`` (both git-ignored).
+``_build/_feedforward.so`` (both git-ignored).  The library needs no torch and is
+put in place first; where torch is without CUDA the binding is left out, and where
+it does not compile a warning says so (the compiler's words are in
+``_build/binding.log``): the operators' calls then go through ctypes.
 ``-Xptxas -v`` resource lines (registers, spills, shared memory per kernel)
 are written next to it in ``ptxas.log``.
 """
@@ -21,6 +24,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -31,6 +35,7 @@ LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 INCLUDE = os.path.join(ROOT, "include")
 BINDING_SOURCE = os.path.join(CSRC, "feedforward_binding.cpp")
 BINDING_PATH = os.path.join(OUT_DIR, "_feedforward.so")
+BINDING_LOG = os.path.join(OUT_DIR, "binding.log")
 
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", *GENCODE, "-Xcompiler", "-fPIC,-O2",
@@ -48,9 +53,12 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _headers():
+    return glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+
+
 def _deps():
-    return (_sources() + [BINDING_SOURCE] + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
+    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + _headers())
 
 
 def _torch_dir():
@@ -60,12 +68,28 @@ def _torch_dir():
     return list(spec.submodule_search_locations)[0] if spec else None
 
 
+def _binding_wanted() -> bool:
+    """Whether torch has the CUDA streams that the binding asks for."""
+    torch_dir = _torch_dir()
+    return bool(torch_dir) and os.path.exists(os.path.join(torch_dir, "lib", "libc10_cuda.so"))
+
+
+def _newer(path: str, deps) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps)
+
+
+def _library_up_to_date() -> bool:
+    return _newer(LIB_PATH, _deps())
+
+
+def _binding_up_to_date() -> bool:
+    """Built, or found not to compile, from what is there now; or not wanted."""
+    deps = [BINDING_SOURCE] + _headers()
+    return not _binding_wanted() or _newer(BINDING_PATH, deps) or _newer(BINDING_LOG, deps)
+
+
 def up_to_date() -> bool:
-    built = [LIB_PATH] + ([BINDING_PATH] if _torch_dir() else [])
-    if not all(os.path.exists(p) for p in built):
-        return False
-    t = min(os.path.getmtime(p) for p in built)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return _library_up_to_date() and _binding_up_to_date()
 
 
 def _compile(src: str) -> tuple[str, str]:
@@ -78,7 +102,7 @@ def _compile(src: str) -> tuple[str, str]:
 
 
 def _compile_binding() -> str:
-    """The binding as a shared object, beside its place until all is built."""
+    """The binding as a shared object, beside its place."""
     torch_dir = _torch_dir()
     headers = os.path.join(torch_dir, "include")
     lib = os.path.join(torch_dir, "lib")
@@ -107,20 +131,35 @@ def _build_lock():
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB_PATH
-    with _build_lock():
-        if not force and up_to_date():  # another process built it while we waited
-            return LIB_PATH
-        return _build_locked(verbose)
+    if force or not up_to_date():
+        with _build_lock():
+            _build_locked(force, verbose)  # what another process built while we waited is not built again
+    if _binding_wanted() and not os.path.exists(BINDING_PATH):
+        warnings.warn("the feed-forward operators' native binding does not build here, so that their calls take the "
+                      f"host longer: see {BINDING_LOG}, and build again with --force", RuntimeWarning, stacklevel=2)
+    return LIB_PATH
 
 
-def _build_locked(verbose: bool) -> str:
-    srcs = _sources()
+def _build_locked(force: bool, verbose: bool) -> None:
+    library = force or not _library_up_to_date()
+    wanted = _binding_wanted() and (force or not _binding_up_to_date())
+    srcs = _sources() if library else []
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
-        binding = ex.submit(_compile_binding) if _torch_dir() else None
+        binding = ex.submit(_compile_binding) if wanted else None
         results = list(ex.map(_compile, srcs))
-        binding_tmp = binding.result() if binding else None
+    if library:
+        _link(results, verbose)
+    if binding:
+        try:
+            os.replace(binding.result(), BINDING_PATH)
+        except Exception as e:  # the library does not need it
+            with open(BINDING_LOG, "w") as f:
+                f.write(f"{e}\n")
+            if os.path.exists(BINDING_PATH):  # of other sources
+                os.remove(BINDING_PATH)
+
+
+def _link(results, verbose: bool) -> None:
     logs = "\n".join(f"== {os.path.basename(o)}\n{err}" for o, err in results)
     with open(os.path.join(OUT_DIR, "ptxas.log"), "w") as f:
         f.write(logs)
@@ -132,9 +171,6 @@ def _build_locked(verbose: bool) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    if binding_tmp:
-        os.replace(binding_tmp, BINDING_PATH)
-    return LIB_PATH
 
 
 def main(argv=None):

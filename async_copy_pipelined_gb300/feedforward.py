@@ -12,7 +12,8 @@ CUDA tensors in, CUDA tensors out, enqueued on `stream` (default: torch's
 current stream) without synchronising.  Ordinary calls (operands on the
 current device, results allocated, no stream given) go through the native
 binding, csrc/feedforward_binding.cpp, which returns None for any other; those,
-and what is to be refused, are dealt with here.
+and what is to be refused, are dealt with here.  Where there is no binding a warning
+says so, and all calls are.
 """
 from __future__ import annotations
 
@@ -21,6 +22,8 @@ import functools
 import importlib.machinery
 import importlib.util
 import os
+import types
+import warnings
 
 from . import training as _t
 
@@ -70,12 +73,26 @@ def _load_native():
     return module
 
 
+def _no_native():
+    """In the native binding's place: leaves every call to Python."""
+    def leave(*args):
+        return None
+    return types.SimpleNamespace(gated_projection=leave, gated_projection_backward=leave, quantize_fp8=leave,
+                                 gemm_fp8=leave)
+
+
 def _load():
     """torch and the native binding, on the first call."""
     global _torch, _bf16, _f32, _native
     if _torch is None:
         torch = _t._load()
-        _native = _load_native()
+        _t._lib()  # without the library there is no call at all
+        try:
+            _native = _load_native()
+        except (RuntimeError, ImportError) as e:
+            warnings.warn(f"{e}.  Calls of the feed-forward operators take the host 10 to 25 us longer without it",
+                          RuntimeWarning, stacklevel=3)
+            _native = _no_native()
         _FORMATS[torch.float8_e4m3fn] = 0  # enum gemm_fp8_format
         _FORMATS[torch.float8_e5m2] = 1
         _bf16, _f32 = torch.bfloat16, torch.float32
