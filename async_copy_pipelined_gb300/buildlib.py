@@ -20,6 +20,7 @@ import fcntl
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -74,6 +75,15 @@ def _binding_wanted() -> bool:
     return bool(torch_dir) and os.path.exists(os.path.join(torch_dir, "lib", "libc10_cuda.so"))
 
 
+def _torch_version() -> str:
+    """The installed torch's, all of it, without importing torch."""
+    try:
+        with open(os.path.join(_torch_dir(), "version.py")) as f:
+            return re.search(r"^__version__ = ['\"]([^'\"]+)['\"]", f.read(), flags=re.M).group(1)
+    except (OSError, AttributeError):
+        return "unknown"
+
+
 def _newer(path: str, deps) -> bool:
     return os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps)
 
@@ -83,9 +93,20 @@ def _library_up_to_date() -> bool:
 
 
 def _binding_up_to_date() -> bool:
-    """Built, or found not to compile, from what is there now; or not wanted."""
-    deps = [BINDING_SOURCE] + _headers()
-    return not _binding_wanted() or _newer(BINDING_PATH, deps) or _newer(BINDING_LOG, deps)
+    """Built, or found not to compile, from what is there now and for the torch
+    that is installed; or not wanted."""
+    if not _binding_wanted():
+        return True
+    if not _newer(BINDING_LOG, [BINDING_SOURCE] + _headers()):
+        return False
+    with open(BINDING_LOG) as f:
+        said = f.readline().strip()
+    return said == _binding_line("failed") or (said == _binding_line("built") and os.path.exists(BINDING_PATH))
+
+
+def _binding_line(outcome: str) -> str:
+    """First line of the binding's log."""
+    return f"torch {_torch_version()}: {outcome}"
 
 
 def up_to_date() -> bool:
@@ -109,7 +130,7 @@ def _compile_binding() -> str:
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     tmp = BINDING_PATH + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-I{INCLUDE}", f"-I{sysconfig.get_paths()['include']}", f"-I{headers}",
+           f'-DBINDING_TORCH="{_torch_version()}"', f"-I{INCLUDE}", f"-I{sysconfig.get_paths()['include']}", f"-I{headers}",
            f"-I{os.path.join(headers, 'torch', 'csrc', 'api', 'include')}", f"-I{cuda}", BINDING_SOURCE, "-o", tmp,
            f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -152,11 +173,13 @@ def _build_locked(force: bool, verbose: bool) -> None:
     if binding:
         try:
             os.replace(binding.result(), BINDING_PATH)
+            said = _binding_line("built")
         except Exception as e:  # the library does not need it
-            with open(BINDING_LOG, "w") as f:
-                f.write(f"{e}\n")
+            said = f"{_binding_line('failed')}\n{e}"
             if os.path.exists(BINDING_PATH):  # of other sources
                 os.remove(BINDING_PATH)
+        with open(BINDING_LOG, "w") as f:
+            f.write(said + "\n")
 
 
 def _link(results, verbose: bool) -> None:

@@ -16,12 +16,14 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <cstring>
+#include <string>
+
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_strided.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
-#include <torch/version.h>
 
 #include "pipelined_ffn.h"
 
@@ -431,10 +433,15 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_feedforward", nullptr, -1, method
 
 } // namespace
 
+// BINDING_TORCH: the whole version of the torch whose headers these are, which its
+// own macro cuts to three numbers, the same for several builds.
 PyMODINIT_FUNC PyInit__feedforward()
 {
+    static const char build[] = BINDING_TORCH;
+    const std::string version(build, std::strcspn(build, "+"));
     PyObject *m = PyModule_Create(&module);
-    if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0)
+    if (m && (PyModule_AddStringConstant(m, "torch_build", build) < 0 ||
+              PyModule_AddStringConstant(m, "torch_version", version.c_str()) < 0))
         Py_CLEAR(m);
     return m;
 }

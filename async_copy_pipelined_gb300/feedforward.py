@@ -63,8 +63,8 @@ def _load_native():
     loader = importlib.machinery.ExtensionFileLoader("_feedforward", _NATIVE_PATH)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_feedforward", loader))
     loader.exec_module(module)
-    if module.torch_version != _t._load().__version__.split("+")[0]:
-        raise RuntimeError(f"native binding was built for torch {module.torch_version}: build it again with "
+    if module.torch_build != str(_t._load().__version__):
+        raise RuntimeError(f"native binding was built for torch {module.torch_build}: build it again with "
                            "`python -m async_copy_pipelined_gb300.buildlib --force`")
     l = _t._lib()
     module.entries(*(ctypes.cast(f, ctypes.c_void_p).value for f in (

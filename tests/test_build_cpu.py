@@ -92,3 +92,35 @@ def test_no_torch_needs_no_binding(tree, monkeypatch, recwarn):
     monkeypatch.setattr(buildlib, "_torch_dir", lambda: None)
     buildlib.build()
     assert _seven() == 7 and _calls(tree) == 0 and buildlib.up_to_date() and not recwarn.list
+
+
+def test_another_torch_is_given_a_binding_of_its_own(tree, monkeypatch):
+    buildlib.build()
+    assert buildlib.up_to_date()
+    (tree / "torch" / "version.py").write_text("__version__ = '1.2.3+two'\n")
+    assert not buildlib.up_to_date()
+    monkeypatch.setattr(buildlib, "_compile", lambda src: pytest.fail("the library was built again"))
+    buildlib.build()
+    assert _calls(tree) == 2 and buildlib.up_to_date()
+
+
+def test_a_binding_that_is_gone_is_built_again(tree):
+    buildlib.build()
+    os.remove(buildlib.BINDING_PATH)
+    assert not buildlib.up_to_date()
+    buildlib.build()
+    assert os.path.exists(buildlib.BINDING_PATH)
+
+
+def test_a_binding_of_another_build_of_the_same_release_is_refused(monkeypatch):
+    import torch
+
+    import async_copy_pipelined_gb300 as pg
+    from async_copy_pipelined_gb300 import feedforward as ff
+    pg.build()
+    assert ff._load_native().torch_build == str(torch.__version__)
+    release = str(torch.__version__).split("+")[0]
+    for other in (release + "+another", release + ".dev20260101+cu130", release + "a0"):
+        monkeypatch.setattr(torch, "__version__", other)
+        with pytest.raises(RuntimeError, match="built for torch"):
+            ff._load_native()
