@@ -189,9 +189,11 @@ def _up_to(n, step):
 
 def _pitch(cols, step):
     """Pitch of new rows of `cols` elements, for `step` elements in 16 bytes:
-    the rows' own length where the next row is aligned, else up to 32 bytes,
-    which are written at once (6606 x 143 x 900 to float32 in 8 bits: 17.6 us at
-    a pitch of 900, 12.1 at 904)."""
+    the rows' own length where that aligns the next row, so that the result is
+    contiguous, else up to 32 bytes, which are written at once (6606 x 143 x 897
+    to float32 in 8 bits: 19.1 us at a pitch of 900, 12.2 at 904).  Rows of an odd
+    number of 16 bytes do without that: 897's neighbour 900 takes 18.7 us at its
+    own length, where 12.2 could be had at 904 by giving the call such a C."""
     return cols if cols % step == 0 else -(-cols // (2 * step)) * 2 * step
 
 
