@@ -33,17 +33,18 @@ constexpr int kEpilogueThreads = 128;
 constexpr uint32_t kWeightBytes = 128 * 128; // of one weight's K block
 constexpr int kMaxRanks = 8;
 constexpr int kAtOnce = 4;
-constexpr int kMaxMaps = 3;
+constexpr int kMaxTokens = 64;
 // Shared memory of one of two CTAs of an SM.  All of it is asked for: it keeps
 // the library's other tensor-core kernels (116 KiB and more) off an SM that has
 // one of these.  Two kernels of clusters, on two streams, that took tensor memory
 // on each other's SMs could otherwise wait for each other in its allocation.
 constexpr int kBudget = 112 * 1024;
 constexpr int kBarrierBytes = 256;
-constexpr int kScaleBytes = 4 * 2 * 128 * 4; // each epilogue warp's tokens' scales of two K blocks
+constexpr int kScaleBytes = 4 * 2 * kMaxTokens * 4; // each epilogue warp's tokens' scales of two K blocks
 
 template <MmaKind Kind, int Tokens>
 struct Shape {
+    static_assert(Tokens <= kMaxTokens, "as many as there is room for scales");
     static constexpr int kWeights = Kind == kMmaF16 ? 2 : 1;
     static constexpr uint32_t kStageBytes = kWeights * kWeightBytes + Tokens * 128;
     static constexpr int kExtra = kBarrierBytes + (Kind == kMmaF8 ? kScaleBytes : 0) + 1024;

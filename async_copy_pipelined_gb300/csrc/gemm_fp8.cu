@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(few_rows::kThreads, 2)
             const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
             // This warp's tokens' scales of two K blocks.
             const uint32_t scales = base + S::kStages * S::kStageBytes + few_rows::kBarrierBytes +
-                                    static_cast<uint32_t>(warp - 2) * (2 * 128 * 4);
+                                    static_cast<uint32_t>(warp - 2) * (2 * few_rows::kMaxTokens * 4);
             constexpr int kPerLane = (Tokens + 31) / 32;
             // Tokens and features outside take the last one's scales.
             const float *from_b =
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(few_rows::kThreads, 2)
             };
             fetch(0);
             for (int f = 0; f < count; ++f) {
-                const uint32_t held = scales + (f & 1) * 512;
+                const uint32_t held = scales + (f & 1) * (few_rows::kMaxTokens * 4);
 #pragma unroll
                 for (int i = 0; i < kPerLane; ++i)
                     if (lane + 32 * i < Tokens)
