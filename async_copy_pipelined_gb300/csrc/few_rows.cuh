@@ -153,8 +153,8 @@ __device__ __forceinline__ void run(const Launch &l, const Maps &maps, uint32_t 
         for (; f < count; ++f) {
             if (f == l.withhold)
                 continue; // test hook: this position is never filled
-            // Together, as in pair_product.cuh.
-            if (__ballot_sync(0xffffffffu, b.ring.producer_acquire(f, l.wait_limit_ns)) != 0xffffffffu) {
+            // Each lane by itself, as in pair_product.cuh.
+            if (!b.ring.producer_acquire(f, l.wait_limit_ns)) {
                 if (on)
                     record_error(l.status, l.family | kErrRoleProducer);
                 break;
@@ -188,7 +188,7 @@ __device__ __forceinline__ void run(const Launch &l, const Maps &maps, uint32_t 
         const uint32_t step = (l.weight_mn ? kMnStep : 32u) >> 4;
         const uint64_t w0 = smem_desc_sw128(base, l.weight_mn ? 8192 : 16, 1024);
         const uint64_t t0 = smem_desc_sw128(base + kWeights * kWeightBytes, 16, 1024);
-        bool ok = true; // of each lane by itself, as in pair_product.cuh
+        bool ok = true;
         for (int f = 0; f < count; ++f) {
             const uint32_t acc = Kind == kMmaF8 ? static_cast<uint32_t>(f & 1) : 0u;
             if (Kind == kMmaF8 &&

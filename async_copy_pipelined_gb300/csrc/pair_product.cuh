@@ -169,10 +169,11 @@ struct Element {
 // and a block's MMAs take 512.  All of the warp runs the loop and one lane
 // issues: with a branch on the lane around the loop the copies' operands are
 // moved to uniform registers one by one, which took longer than a block's MMAs
-// (8192 x 4096 by two 4096 x 8192: 741 us, like this 595).  Lanes find each for
-// itself whether a wait has run out, and go on or give up together: a lane that left
-// alone would miss at the others' next meeting (a ballot, which costs nothing here;
-// __all_sync takes 1 % of the 8-bit product by columns).
+// (8192 x 4096 by two 4096 x 8192: 741 us, like this 595).
+//
+// A lane whose wait has run out leaves the loops alone, so nothing in them may need
+// all lanes: what counts is the one that issues, and each comes to the loops' end by
+// its own waits.
 template <MmaKind Kind, bool IsB>
 __device__ __forceinline__ void produce(const Launch &l, const Maps &maps, const Barriers &b, uint32_t base, int rank,
                                         uint32_t leader, int first, int stride)
@@ -202,7 +203,7 @@ __device__ __forceinline__ void produce(const Launch &l, const Maps &maps, const
             for (int kb = begin; kb < end; ++kb, ++f) {
                 if (static_cast<int>(f) == l.withhold)
                     continue; // test hook: this position is never filled
-                if (__ballot_sync(0xffffffffu, b.ring.producer_acquire(f, l.wait_limit_ns)) != 0xffffffffu) {
+                if (!b.ring.producer_acquire(f, l.wait_limit_ns)) {
                     if (on)
                         record_error(l.status, l.family | kErrRoleProducer);
                     ok = false;
@@ -248,10 +249,8 @@ __device__ __forceinline__ void produce(const Launch &l, const Maps &maps, const
 // The MMA warp of rank 0.  PerBlock: every K block has an accumulator of its
 // own, which the epilogue scales and adds up; otherwise every tile has.
 //
-// A lane whose wait has run out leaves the loops alone.  What counts is the one that
-// issues, and nothing here needs all lanes, so each comes to the loops' end by its
-// own waits.  (A vote between the waits and the MMAs: 8192 cubed in 8 bits 389 -> 412
-// us, a ballot 401, one vote a tile 395.)
+// Lanes leave the loops as the producers' do.  (A vote between the waits and the MMAs:
+// 8192 cubed in 8 bits 389 -> 412 us, a ballot 401, one vote a tile 395.)
 template <MmaKind Kind, bool PerBlock>
 __device__ __forceinline__ void multiply(const Launch &l, const Barriers &b, uint32_t base, uint32_t tmem,
                                          uint32_t leader, int first, int stride)
