@@ -13,10 +13,11 @@
 // dx with two segments of K blocks (dG Wg^T, then dU Wu^T, one sum), dWg and
 // dWu as one product whose tile takes 128 columns of each.
 //
-// Measured: 8192 x 4096 -> 8192 in 571 us (1.93 PFLOP/s), 590 with G and U kept,
-// under the power limit like the library product of that size (520 to 540); its
-// gradient in 1300 (2.2 TFLOP; 95 of them dG and dU, 7 TB/s).  One token 23 us, 5.8
-// TB/s of the weights.
+// Measured, call after call for seconds, where the power limit holds: 8192 x 4096 ->
+// 8192 in 667 us (1.65 PFLOP/s), 698 with G and U kept, where a library product of that
+// size takes 622; its gradient in 1500 (2.2 TFLOP; 95 us of them dG and dU, 7 TB/s),
+// where library products of its sizes take 1305.  In a burst of six calls 604, 630
+// (570), 1370 (1196).  One token 23 us on the device, 5.8 TB/s of the weights.
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
@@ -226,7 +227,9 @@ struct Slopes {
     int counters;
 };
 
-// dG and dU, eight columns a thread.
+// dG and dU, eight columns a thread, computed in float32 and rounded to bfloat16: they
+// are operands of the tensor cores.  With the result's own rounding a gradient is off
+// by 0.0024 of its norm, where one rounding alone gives 0.0017.
 constexpr int kSlopeThreads = 256;
 
 // Eight elements in pieces of Bytes, to which their address is aligned.

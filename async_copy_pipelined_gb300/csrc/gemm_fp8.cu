@@ -13,9 +13,10 @@
 // only after the commit's way to the epilogue, the epilogue's reading (450) and the
 // arrival's way back, and there are two: about 790 a block.  A scale for each
 // column of B costs a second FMA-pipe instruction for every two sums, and about
-// 1200.  8192 cubed with a scale per 128 x 128 of B 390 us (2.82 PFLOP/s), with one
-// for each column 560; 4096 cubed 70, 4096 x 8192 x 4096 by columns 169.  One token by
-// 8192 x 4096: 10 us, 3.4 TB/s.
+// 1200.  8192 cubed with a scale per 128 x 128 of B 441 us call after call for seconds,
+// under the power limit (2.49 PFLOP/s), in some tens of calls 390, with one for each
+// column 564; 4096 cubed 70, 4096 x 4096 x 8192 by columns 172.  One token by 8192 x
+// 4096: 10 us, 3.4 TB/s.
 //
 // Few tiles and a long contraction: the pairs of a cluster share a tile's K blocks and
 // join their sums through shared memory (splits_for).
